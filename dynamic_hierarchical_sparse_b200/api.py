@@ -35,7 +35,8 @@ EXPORTED = [
     "dhsa_attention_workspace_size", "dhsa_attention", "dhsa_workspace_status",
     "dhsa_selftest_timeout", "dhsa_plan_noalloc", "dhsa_attention_kv_plan",
     "dhsa_segment_capacity", "dhsa_segment_workspace_size", "dhsa_segment", "dhsa_plan_check",
-    "dhsa_plan_margins",
+    "dhsa_plan_margins", "dhsa_rope_init", "dhsa_rope_init_freq", "dhsa_rope", "dhsa_kv_append",
+    "dhsa_paged_attention_workspace_size", "dhsa_paged_attention",
 ]
 
 DHSA_BUDGET_PER_KV_HEAD = 0x100
@@ -65,6 +66,38 @@ class _Problem(ctypes.Structure):
 
 class _SegmentRule(ctypes.Structure):
     _fields_ = [("threshold", ctypes.c_float), ("min_len", ctypes.c_int32), ("max_len", ctypes.c_int32)]
+
+
+ROPE_MAX_PAIRS = 128
+ROPE_KINDS = {"linear": 1, "llama3": 2, "yarn": 3}
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class _RopeTable(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class _Tokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("group_ptr", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("h_cu_q", ctypes.c_void_p), ("h_group_ptr", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -106,6 +139,12 @@ def lib() -> ctypes.CDLL:
             "dhsa_segment": (ctypes.c_int, [P, I32, I32, I32, I32, P, P, _SegmentRule, P, I64, P, P, P, SZ, P]),
             "dhsa_plan_check": (ctypes.c_int, [PP, P, P, I64, I32, P, SZ, P]),
             "dhsa_plan_margins": (ctypes.c_int, [PP, _Budget, P, P, I64, P, SZ, P, P]),
+            "dhsa_rope_init": (ctypes.c_int, [P, I32, I32, ctypes.c_double, P]),
+            "dhsa_rope_init_freq": (ctypes.c_int, [P, I32, I32, P, ctypes.c_double]),
+            "dhsa_rope": (ctypes.c_int, [P, I32, I32, I32, P, _Tokens, I32, _Tokens, _Tokens, I32, _Tokens, P]),
+            "dhsa_kv_append": (ctypes.c_int, [P, P, P, P, _Tokens, _Tokens, _Tokens, _Tokens, _Tokens, I32, P, SZ, P]),
+            "dhsa_paged_attention_workspace_size": (ctypes.c_int, [P, P, I32, ctypes.POINTER(SZ)]),
+            "dhsa_paged_attention": (ctypes.c_int, [P, P, _Tokens, I32, ctypes.c_float, _Tokens, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -440,3 +479,314 @@ def selftest_timeout(limit_us: int = 20000, device=None) -> int:
     st = _stream_ptr(None)
     _check(lib().dhsa_selftest_timeout(_ptr(ws), int(limit_us), st), "dhsa_selftest_timeout")
     return int(lib().dhsa_workspace_status(_ptr(ws), st))
+
+
+# ------------------------------------------------- around the prefill path
+
+
+class _on_device:
+    """Makes a tensor's device the current one for a call (launches and the
+    current stream go by it); nothing to do where it already is."""
+
+    def __init__(self, t: torch.Tensor):
+        self.index = t.device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dtype: torch.dtype, tokens: int,
+            device: torch.device) -> _Tokens:
+    """A packed [T, H, d] operand whose tokens may lie apart (a slice of a fused tensor)."""
+    if t is None:
+        return _Tokens(None, 0)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, the call on %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    s = t.shape
+    if len(s) != 3 or s[0] < tokens or s[1] != heads or s[2] != head_dim:
+        raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(s)))
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    return _Tokens(t.data_ptr(), st[0] if s[0] > 1 else heads * head_dim)
+
+
+def _int32(t: torch.Tensor, name: str, shape, device: torch.device) -> None:
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be int32" % name)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+class Rope:
+    """Rotary frequencies (dhsa_rope_table): host data, usable on any device.
+
+    ``rotary_dim``: the first numbers of a head that turn; pairs are (i, i +
+    rotary_dim / 2), or (2i, 2i + 1) when ``interleaved``.  ``scaling``: a
+    ``workloads.RopeScaling`` or None.  ``inv_freq`` gives the rotary_dim / 2
+    frequencies themselves (then ``base`` and ``scaling`` are not used), with
+    ``factor`` on cos and sin."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling=None,
+                 inv_freq=None, factor: float = 1.0):
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
+        self.c = _RopeTable()
+        if inv_freq is not None:
+            f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+            if f.shape != (self.rotary_dim // 2,):
+                raise ValueError("inv_freq must have rotary_dim / 2 entries")
+            _check(lib().dhsa_rope_init_freq(ctypes.byref(self.c), self.rotary_dim, int(self.interleaved),
+                                             f.ctypes.data_as(ctypes.c_void_p), float(factor)), "dhsa_rope_init_freq")
+            return
+        sc = None
+        if scaling is not None:
+            if scaling.kind not in ROPE_KINDS:
+                raise ValueError("unknown rope scaling %r" % (scaling.kind,))
+            sc = ctypes.byref(_RopeScaling(ROPE_KINDS[scaling.kind], scaling.factor, scaling.original_len,
+                                           scaling.low_freq_factor, scaling.high_freq_factor, scaling.beta_fast,
+                                           scaling.beta_slow))
+        _check(lib().dhsa_rope_init(ctypes.byref(self.c), self.rotary_dim, int(self.interleaved), float(base), sc),
+               "dhsa_rope_init")
+
+
+def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, rope: Rope,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotates packed q [T, Hq, d] and k [T, Hkv, d] (either may be None) at
+    ``positions`` (int32 [T]); returns (q_out, k_out).  Outputs are made where
+    they are not given; an output may be its own input."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("rope needs q or k")
+    T, d, dev = x.shape[0], x.shape[-1], x.device
+    _int32(positions, "positions", (T,), dev)
+    dt = _dtype_code(x)
+    with _on_device(x):
+        args = []
+        outs = []
+        for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+            if t is None:
+                if out is not None:
+                    raise ValueError("%s_out without %s" % (name, name))
+                args += [_Tokens(None, 0), 1, _Tokens(None, 0)]
+                outs.append(None)
+                continue
+            H = t.shape[1]
+            if out is None:
+                out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
+            args += [_tokens(t, name, H, d, x.dtype, T, dev), H, _tokens(out, name + "_out", H, d, x.dtype, T, dev)]
+            outs.append(out)
+        _enter(stream)
+        _check(lib().dhsa_rope(ctypes.byref(rope.c), dt, d, T, _ptr(positions), *args, _stream_ptr(stream)),
+               "dhsa_rope")
+        _leave(stream)
+    return tuple(outs)
+
+
+class PagedCache:
+    """The pages of a K/V cache: ``k_pages`` and ``v_pages`` [pages, Hkv,
+    page_size, d] on the device, each page contiguous (pages may lie apart, by
+    the same stride in both).  K in bf16 and V in f16, or both in fp32."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not t.is_cuda or t.dim() != 4:
+                raise ValueError("%s must be a CUDA tensor [pages, Hkv, page_size, d]" % name)
+        if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must have one shape and device")
+        want = {torch.bfloat16: torch.float16, torch.float32: torch.float32}.get(k_pages.dtype)
+        if want is None or v_pages.dtype != want:
+            raise TypeError("pages must be K bfloat16 with V float16, or both float32; got %s, %s"
+                            % (k_pages.dtype, v_pages.dtype))
+        n, h, p, d = k_pages.shape
+        for t in (k_pages, v_pages):
+            st = t.stride()
+            if st[3] != 1 or (p > 1 and st[2] != d) or (h > 1 and st[1] != p * d):
+                raise ValueError("a page must be contiguous")
+        if n > 1 and k_pages.stride(0) != v_pages.stride(0):
+            raise ValueError("k_pages and v_pages must have one page stride")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = n, h, p, d
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.c = _PagedCache(_dtype_code(k_pages), h, d, p, n, k_pages.stride(0) if n > 1 else h * p * d,
+                             k_pages.data_ptr(), v_pages.data_ptr())
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, dtype: torch.dtype,
+              device=None) -> "PagedCache":
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        v_dtype = torch.float16 if dtype == torch.bfloat16 else dtype
+        return PagedCache(torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=v_dtype, device=dev))
+
+
+class PagedBatch:
+    """One step of a batch over a paged cache (dhsa_paged_batch).
+
+    ``cu_q``: host offsets [B+1] of the sequences' new tokens in the packed
+    tensors; ``kv_lens`` int32 [B] on the device: tokens a sequence holds with
+    them; ``block_table`` int32 [B, max_pages] on the device.  ``group_ptr``
+    (host [G+1]) and ``prefix_lens`` (int32 [G] on the device): the sequences of
+    a group share their first prefix_lens[g] tokens.  The device tensors are
+    kept and read by every call, so a program may go on writing them."""
+
+    def __init__(self, cu_q, kv_lens: torch.Tensor, block_table: torch.Tensor, group_ptr=None,
+                 prefix_lens: Optional[torch.Tensor] = None):
+        self.h_cu = np.ascontiguousarray(np.asarray(cu_q, dtype=np.int32))
+        if self.h_cu.ndim != 1 or self.h_cu.shape[0] < 1:
+            raise ValueError("cu_q must have B + 1 entries")
+        self.num_seqs = int(self.h_cu.shape[0] - 1)
+        self.total_tokens = int(self.h_cu[-1])
+        dev = kv_lens.device
+        _int32(kv_lens, "kv_lens", (self.num_seqs,), dev)
+        if not block_table.is_cuda or block_table.device != dev or block_table.dtype != torch.int32:
+            raise ValueError("block_table must be an int32 tensor on %s" % dev)
+        if block_table.dim() != 2 or block_table.shape[0] != self.num_seqs or block_table.shape[1] < 1 or \
+                block_table.stride(1) != 1:
+            raise ValueError("block_table must be [B, max_pages] with contiguous rows")
+        if (group_ptr is None) != (prefix_lens is None):
+            raise ValueError("group_ptr and prefix_lens come together")
+        width = int(block_table.shape[1])
+        stride = int(block_table.stride(0)) if self.num_seqs > 1 else width
+        self.device, self.kv_lens, self.block_table, self.prefix_lens = dev, kv_lens, block_table, prefix_lens
+        self.d_cu = torch.from_numpy(self.h_cu).to(dev)
+        groups, self.h_groups, self.d_groups = 0, None, None
+        if group_ptr is not None:
+            self.h_groups = np.ascontiguousarray(np.asarray(group_ptr, dtype=np.int32))
+            groups = int(self.h_groups.shape[0] - 1)
+            if groups < 1:
+                raise ValueError("group_ptr must have G + 1 entries, G >= 1")
+            _int32(prefix_lens, "prefix_lens", (groups,), dev)
+            self.d_groups = torch.from_numpy(self.h_groups).to(dev)
+        self.c = _PagedBatch(self.num_seqs, width, stride, groups, self.d_cu.data_ptr(), kv_lens.data_ptr(),
+                             block_table.data_ptr(), 0 if groups == 0 else self.d_groups.data_ptr(),
+                             0 if groups == 0 else prefix_lens.data_ptr(), self.h_cu.ctypes.data,
+                             0 if groups == 0 else self.h_groups.ctypes.data)
+
+
+class KvAppender:
+    """Repeated dhsa_kv_append calls over one cache, batch and rotation (None:
+    keys are stored as they come).  Owns the status word, which gathers reports
+    until ``reset``.  Stream ordering as for Planner."""
+
+    def __init__(self, cache: PagedCache, batch: PagedBatch, rope: Optional[Rope] = None):
+        if cache.device != batch.device:
+            raise ValueError("cache and batch are on different devices")
+        self.cache, self.batch, self.rope = cache, batch, rope
+        self.ws = torch.zeros(256, dtype=torch.uint8, device=cache.device)
+        self._refs = (ctypes.byref(cache.c), ctypes.byref(batch.c), None if rope is None else ctypes.byref(rope.c))
+
+    def __call__(self, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, stream=None):
+        """Stores k and v [T, Hkv, d]; returns (q_out, k_out): q [T, Hq, d]
+        rotated (made where q comes without q_out) and, where given, k_out."""
+        c, T = self.cache, self.batch.total_tokens
+        hq, d, dt, dev = (1 if q is None else q.shape[1]), c.head_dim, c.dtype, c.device
+        if q is None and q_out is not None:
+            raise ValueError("q_out without q")
+        if positions is not None:
+            _int32(positions, "positions", (T,), dev)
+        with _on_device(self.ws):
+            if q is not None and q_out is None:
+                q_out = torch.empty(T, hq, d, dtype=dt, device=dev)
+            _check(lib().dhsa_kv_append(
+                self._refs[0], self._refs[1], self._refs[2], _ptr(positions),
+                _tokens(k, "k", c.num_kv_heads, d, dt, T, dev), _tokens(v, "v", c.num_kv_heads, d, dt, T, dev),
+                _tokens(k_out, "k_out", c.num_kv_heads, d, dt, T, dev), _tokens(q, "q", hq, d, dt, T, dev),
+                _tokens(q_out, "q_out", hq, d, dt, T, dev), hq, _ptr(self.ws), 256, _stream_ptr(stream)),
+                "dhsa_kv_append")
+        return q_out, k_out
+
+    def status(self, stream=None) -> int:
+        with _on_device(self.ws):
+            return lib().dhsa_workspace_status(_ptr(self.ws), _stream_ptr(stream))
+
+    def reset(self) -> None:
+        """Clears the status word (on the current stream)."""
+        self.ws.zero_()
+
+
+def append_kv(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, stream=None,
+              check: bool = False):
+    """One-shot append to the paged cache; returns (q_out, k_out) as KvAppender does."""
+    a = KvAppender(cache, batch, rope)
+    with _on_device(a.ws):
+        _enter(stream)
+        if q is not None and q_out is None:
+            q_out = torch.empty(batch.total_tokens, q.shape[1], cache.head_dim, dtype=cache.dtype,
+                                device=cache.device)
+        out = a(k, v, q, q_out, k_out, positions, stream)
+        if check:
+            _check(a.status(stream), "dhsa_kv_append (device)")
+        _leave(stream)
+    return out
+
+
+class PagedAttention:
+    """Repeated dhsa_paged_attention calls over one cache, batch and number of
+    query heads.  Owns the workspace (status word included, which gathers
+    reports until ``reset``).  Stream ordering as for Planner."""
+
+    def __init__(self, cache: PagedCache, batch: PagedBatch, num_q_heads: int):
+        if cache.device != batch.device:
+            raise ValueError("cache and batch are on different devices")
+        self.cache, self.batch, self.num_q_heads = cache, batch, int(num_q_heads)
+        n = ctypes.c_size_t(0)
+        _check(lib().dhsa_paged_attention_workspace_size(ctypes.byref(cache.c), ctypes.byref(batch.c),
+                                                         self.num_q_heads, ctypes.byref(n)),
+               "dhsa_paged_attention_workspace_size")
+        self.ws = _workspace(n.value, cache.device)
+        self.reset()
+        self._refs = (ctypes.byref(cache.c), ctypes.byref(batch.c))
+
+    def __call__(self, q: torch.Tensor, out: torch.Tensor, scale: Optional[float] = None,
+                 lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        c, T, hq = self.cache, self.batch.total_tokens, self.num_q_heads
+        dev = c.device
+        if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous()
+                                or lse.dim() != 2 or lse.shape[0] < T or lse.shape[1] != hq):
+            raise ValueError("lse must be a contiguous float32 [>= %d, %d] tensor on %s" % (T, hq, dev))
+        with _on_device(self.ws):
+            _check(lib().dhsa_paged_attention(
+                self._refs[0], self._refs[1], _tokens(q, "q", hq, c.head_dim, c.dtype, T, dev), hq,
+                0.0 if scale is None else scale, _tokens(out, "out", hq, c.head_dim, c.dtype, T, dev), _ptr(lse),
+                _ptr(self.ws), self.ws.numel(), _stream_ptr(stream)), "dhsa_paged_attention")
+        return out
+
+    def status(self, stream=None) -> int:
+        with _on_device(self.ws):
+            return lib().dhsa_workspace_status(_ptr(self.ws), _stream_ptr(stream))
+
+    def reset(self) -> None:
+        """Clears the status word (on the current stream)."""
+        self.ws[:256].zero_()
+
+
+def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, scale: Optional[float] = None,
+                    lse: Optional[torch.Tensor] = None, stream=None, check: bool = False) -> torch.Tensor:
+    """Attention of the new tokens q [T, Hq, d] over the paged cache.  Rows of
+    the result behind the last sequence's are zero."""
+    a = PagedAttention(cache, batch, q.shape[1])
+    with _on_device(a.ws):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out[batch.total_tokens:].zero_()
+        _enter(stream)
+        a(q, out, scale, lse, stream)
+        if check:
+            _check(a.status(stream), "dhsa_paged_attention (device)")
+        _leave(stream)
+    return out

@@ -16,23 +16,26 @@
 
 namespace dhsa {
 
-// 3-D (d, heads, tokens) view of a packed THD bf16 tensor with a (64, 1,
-// box_rows) box and 128-byte swizzle: one box lands as box_rows x 128 bytes,
-// the canonical K-major SW128 operand layout of tcgen05.mma.
-CUresult encode_qkv_map(CUtensorMap* map, const void* base, int heads, int head_dim, int tokens, int box_rows,
-                        bool f16) {
-  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static EncodeFn fn = nullptr;
+TensorMapEncodeFn tensor_map_encode_fn() {
+  static TensorMapEncodeFn fn = nullptr;
   if (fn == nullptr) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess || p == nullptr)
-      return CUDA_ERROR_NOT_FOUND;
-    fn = reinterpret_cast<EncodeFn>(p);
+      return nullptr;
+    fn = reinterpret_cast<TensorMapEncodeFn>(p);
   }
+  return fn;
+}
+
+// 3-D (d, heads, tokens) view of a packed THD bf16 tensor with a (64, 1,
+// box_rows) box and 128-byte swizzle: one box lands as box_rows x 128 bytes,
+// the canonical K-major SW128 operand layout of tcgen05.mma.
+CUresult encode_qkv_map(CUtensorMap* map, const void* base, int heads, int head_dim, int tokens, int box_rows,
+                        bool f16) {
+  const TensorMapEncodeFn fn = tensor_map_encode_fn();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,

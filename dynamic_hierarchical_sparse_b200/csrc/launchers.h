@@ -73,6 +73,12 @@ cudaError_t launch_attention_bf16(const AttnBf16Args& a, cudaStream_t stream);
 cudaError_t launch_attention_pair(const AttnBf16Args& a, cudaStream_t stream);
 // head_dim 256: one query tile per CTA, 128-key tiles, S double-buffered and P in TMEM.
 cudaError_t launch_attention_d256(const AttnBf16Args& a, cudaStream_t stream);
+// The driver's cuTensorMapEncodeTiled (looked up once), or null.
+using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                       CUtensorMapFloatOOBfill);
+TensorMapEncodeFn tensor_map_encode_fn();
 // TMA view of a packed THD bf16 tensor (see attention_bf16.cu).
 CUresult encode_qkv_map(CUtensorMap* map, const void* base, int heads, int head_dim, int tokens, int box_rows,
                         bool f16 = false);

@@ -1,0 +1,253 @@
+// The work list of paged attention, shared by its kernels: items, segments,
+// pieces, and where their partial results lie (see PagedWork in serving.h).
+#pragma once
+
+#include "common.cuh"
+#include "serving.h"
+
+namespace dhsa {
+
+// One item: the query tokens [t0, t1) over the keys [lo, hi) of a table row.
+struct PagedItem {
+  int t0, t1, lo, hi, row;
+};
+
+__device__ __forceinline__ int paged_clamp_len(const PagedArgs& p, int n) {
+  return min(max(n, 0), p.max_pages * p.page_size);
+}
+
+// The group that holds sequence b (the last g with group_ptr[g] <= b).
+__device__ __forceinline__ int paged_group_of(const PagedArgs& p, int b) {
+  int lo = 0, hi = p.num_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.group_ptr[mid] <= b) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The sequence that brings token t < total_q.
+__device__ __forceinline__ int paged_seq_of(const PagedArgs& p, int t) {
+  if (p.uniform_q > 0) return t / p.uniform_q;
+  int lo = 0, hi = p.num_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_q[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Keys visible to token t of sequence b.
+__device__ __forceinline__ int paged_limit(const PagedArgs& p, int b, int t) {
+  return paged_clamp_len(p, p.kv_lens[b]) - (p.cu_q[b + 1] - 1 - t);
+}
+
+// Item i: the groups come first, then the sequences.  `groups`: num_groups, or
+// 0 where the caller's list holds the sequences alone.
+__device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, int i, int groups) {
+  PagedItem it;
+  if (i < groups) {
+    const int s0 = min(max(p.group_ptr[i], 0), p.num_seqs), s1 = min(max(p.group_ptr[i + 1], s0), p.num_seqs);
+    it.t0 = p.cu_q[s0];
+    it.t1 = p.cu_q[s1];
+    it.lo = 0;
+    it.hi = paged_clamp_len(p, p.prefix_lens[i]);
+    it.row = s0;
+    if (s0 == s1) it.hi = 0;
+  } else {
+    const int b = i - groups;
+    it.t0 = p.cu_q[b];
+    it.t1 = p.cu_q[b + 1];
+    it.hi = paged_clamp_len(p, p.kv_lens[b]);
+    it.lo = p.num_groups > 0 ? min(paged_clamp_len(p, p.prefix_lens[paged_group_of(p, b)]), it.hi) : 0;
+    it.row = b;
+  }
+  return it;
+}
+
+// Rows of one segment's tile: a power of two from 16 to kMax that the item's
+// rows fill, so that few rows (one decode step of one sequence) take the form
+// in which all four warps split the keys, and many are worked on together.
+template <int kMax>
+__host__ __device__ __forceinline__ int paged_tile_rows(int rows) {
+  int m = 16;
+  while (m < kMax && m < rows) m *= 2;
+  return m;
+}
+
+// An item's segments and key tiles.
+template <int BN, int kMaxRows>
+struct PagedSpan {
+  int rows, tm, rt, first, nt;  // rows; rows a tile, row tiles; first key tile, key tiles
+  __device__ __forceinline__ PagedSpan(const PagedItem& it, int group_heads) {
+    rows = (it.t1 - it.t0) * group_heads;
+    tm = paged_tile_rows<kMaxRows>(rows);
+    rt = (rows + tm - 1) / tm;
+    first = it.lo / BN;
+    nt = it.hi > it.lo && rows > 0 ? (it.hi + BN - 1) / BN - first : 0;
+  }
+  __device__ __forceinline__ long long units(int num_kv_heads) const {
+    return static_cast<long long>(num_kv_heads) * rt * nt;
+  }
+  __device__ __forceinline__ long long part_rows(int num_kv_heads) const {
+    return static_cast<long long>(num_kv_heads) * rt * tm;
+  }
+};
+
+// First unit (key tile of the whole list) of CTA c, and the CTA that holds a
+// unit.  With fewer units than CTAs the first `total` CTAs take one each, so
+// every CTA between the first and the last owner of a segment has a partial of it.
+__device__ __forceinline__ int paged_ctas(long long total, int ctas) {
+  return static_cast<int>(min(total, static_cast<long long>(ctas)));
+}
+__device__ __forceinline__ long long paged_first_unit(long long c, long long total, int ctas) {
+  const int n = paged_ctas(total, ctas);
+  return c < n ? c * total / n : total;
+}
+__device__ __forceinline__ int paged_owner(long long unit, long long total, int ctas) {
+  return static_cast<int>(((unit + 1) * paged_ctas(total, ctas) - 1) / total);
+}
+
+// Where CTA c's partial of a segment starts (rows): c steps by the largest
+// tile, a segment by its own, and along the list either c or the segment moves
+// on, so no two partials overlap.
+__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int tm) {
+  return static_cast<long long>(c) * max_rows + item_row + static_cast<long long>(seg) * tm;
+}
+
+// Shared-memory words of the block-wide scan.
+struct PagedScan {
+  long long warp_units[32], warp_rows[32];
+  long long total, item_unit, item_row;
+  int item;
+};
+
+// Every CTA counts the units of all items (each thread a run of them) and finds
+// the item that holds its first unit.  CTA 0 writes the items' first units and
+// rows for the merge.  kThreads threads, all of them call this.
+template <int BN, int kMaxRows, int kThreads>
+__device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_heads, int groups, long long* items,
+                                               PagedScan* sc, uint32_t* status) {
+  const int n = groups + p.num_seqs;
+  const int per = (n + kThreads - 1) / kThreads;
+  const int i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
+  long long units = 0, rows = 0;
+  bool bad = false;
+  for (int i = i0; i < i1; ++i) {
+    const PagedItem it = paged_item(p, i, groups);
+    const PagedSpan<BN, kMaxRows> sp(it, group_heads);
+    units += sp.units(p.num_kv_heads);
+    rows += sp.part_rows(p.num_kv_heads);
+    if (blockIdx.x == 0) {
+      if (i < groups) {
+        bad |= it.t1 > it.t0 && p.prefix_lens[i] != paged_clamp_len(p, p.prefix_lens[i]);
+      } else {
+        bad |= p.kv_lens[i - groups] != it.hi;
+      }
+    }
+  }
+  if (bad) report(status, kDevCheck);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long iu = units, ir = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const long long u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
+    if (lane >= o) {
+      iu += u;
+      ir += r;
+    }
+  }
+  if (lane == 31) {
+    sc->warp_units[warp] = iu;
+    sc->warp_rows[warp] = ir;
+  }
+  __syncthreads();
+  long long base_u = iu - units, base_r = ir - rows, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long u = sc->warp_units[w];
+    if (w < warp) {
+      base_u += u;
+      base_r += sc->warp_rows[w];
+    }
+    total += u;
+  }
+  const long long mine = paged_first_unit(blockIdx.x, total, gridDim.x);
+  if (threadIdx.x == 0) sc->total = total;
+  const bool find = units > 0 && base_u <= mine && mine < base_u + units;
+  if (find || blockIdx.x == 0) {
+    long long u = base_u, r = base_r;
+    for (int i = i0; i < i1; ++i) {
+      const PagedItem it = paged_item(p, i, groups);
+      const PagedSpan<BN, kMaxRows> sp(it, group_heads);
+      const long long du = sp.units(p.num_kv_heads);
+      if (du > 0 && u <= mine && mine < u + du) {
+        sc->item = i;
+        sc->item_unit = u;
+        sc->item_row = r;
+      }
+      if (blockIdx.x == 0) {
+        items[i] = u;
+        items[n + 1 + i] = r;
+      }
+      u += du;
+      r += sp.part_rows(p.num_kv_heads);
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) items[n] = total;
+  __syncthreads();
+}
+
+// A CTA's walk over its pieces: consecutive key tiles of one segment each.
+template <int BN, int kMaxRows>
+struct PagedWalk {
+  const PagedArgs* p;
+  int group_heads, groups;
+  int i;
+  PagedItem it;
+  int tm, rt, first, nt;
+  long long item_row, left;
+  int seg, kt, count;  // current piece: segment, first key tile (of the item), tiles
+
+  __device__ __forceinline__ void load() {
+    it = paged_item(*p, i, groups);
+    const PagedSpan<BN, kMaxRows> sp(it, group_heads);
+    tm = sp.tm;
+    rt = sp.rt;
+    first = sp.first;
+    nt = sp.nt;
+  }
+  // false: no work for this CTA
+  __device__ __forceinline__ bool init(const PagedArgs* args, int gh, int ngroups, const PagedScan* sc) {
+    p = args;
+    group_heads = gh;
+    groups = ngroups;
+    const long long u0 = paged_first_unit(blockIdx.x, sc->total, gridDim.x);
+    left = paged_first_unit(blockIdx.x + 1, sc->total, gridDim.x) - u0;
+    if (left <= 0) return false;
+    i = sc->item;
+    item_row = sc->item_row;
+    load();
+    const long long off = u0 - sc->item_unit;
+    seg = static_cast<int>(off / nt);
+    kt = static_cast<int>(off - static_cast<long long>(seg) * nt);
+    count = static_cast<int>(min(static_cast<long long>(nt - kt), left));
+    return true;
+  }
+  __device__ __forceinline__ bool next() {
+    left -= count;
+    if (left <= 0) return false;
+    kt = 0;
+    if (++seg == p->num_kv_heads * rt) {
+      seg = 0;
+      do {
+        item_row += static_cast<long long>(p->num_kv_heads) * rt * tm;
+        if (++i >= groups + p->num_seqs) return false;
+        load();
+      } while (nt == 0);
+    }
+    count = static_cast<int>(min(static_cast<long long>(nt), left));
+    return true;
+  }
+};
+
+}  // namespace dhsa

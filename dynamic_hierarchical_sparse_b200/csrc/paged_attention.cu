@@ -1,0 +1,796 @@
+// Attention of new query tokens over a paged cache: a shared prefix is read once
+// for the rows of all the sequences that share it, then every sequence's own
+// keys, and a last kernel joins the partial results of each row.
+//
+//   out[t, h] = sum_{s < L} exp(x_s - m) v_s / l,  x_s = q . k_s * scale,
+//   l = sum_s exp(x_s - m)
+// is associative over sets of keys: a set's (m, l, O = sum exp(x - m) v) joins
+// with another's by scaling both to the larger m.  So the key tiles of all
+// items (prefixes with all their group's rows, sequences with their own) form
+// one list that is cut evenly among the CTAs, wherever that falls, and every
+// CTA leaves (m, l, O) for each segment that it touches.
+//
+// paged_mma_kernel (bf16): bound by HBM as long as a tile's rows are few.  One
+// warp brings 64-key tiles of K and V from the pages by TMA (128-byte swizzle)
+// into a ring, ahead across pieces; four warps run S = Q K^T and O += P V on
+// mma.sync m16n8k16 fragments.  With 16 rows or fewer the four warps split a
+// tile's keys (each with its own running max and O, joined when the piece
+// ends), with 32 two split them, with 64 every warp has 16 rows of its own.
+// Q stays in registers, P goes from the S fragments straight into the A
+// operand of P V (f16, as V).
+//
+// paged_f32_kernel (fp32): the same list in FFMA, 32-key tiles by cp.async.
+#include "launchers.h"
+#include "paged.cuh"
+
+namespace dhsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ bf16
+constexpr int kBN = 64;        // keys a tile
+constexpr int kMaxRows = 64;   // rows a tile at most
+constexpr int kMmaThreads = 160;  // four compute warps, one producer
+constexpr int kProducer = 4;
+
+template <int D>
+struct MmaCfg {
+  static constexpr int kSlices = D / 64;             // 64-column (128-byte) slices of a row
+  static constexpr int kTileBytes = kBN * D * 2;     // one K or V tile
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kCtas = D == 64 ? 3 : D == 128 ? 2 : 1;  // resident on an SM
+  static constexpr int kJoinStride = D / 4 + 8;      // floats; + 8: the fragment writes of a half-warp hit all banks
+  static constexpr int kOffJoin = kStages * 2 * kTileBytes;
+  static constexpr int kOffMl = kOffJoin + 4 * 16 * kJoinStride * 4;
+  static constexpr int kOffScan = kOffMl + 4 * 16 * 8;
+  static constexpr int kOffBar = kOffScan + ((static_cast<int>(sizeof(PagedScan)) + 15) / 16) * 16;
+  static constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16 + 1024;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
+};
+
+// 4-D tiled load (no multicast) into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct MmaCtx {
+  uint32_t sbase, bar0;
+  unsigned char* smem;
+  volatile int* abort_flag;
+  int stage;
+  uint32_t phase;
+};
+
+__device__ __forceinline__ uint32_t bar_full(const MmaCtx& c, int s) { return c.bar0 + 8u * s; }
+template <int kStages>
+__device__ __forceinline__ uint32_t bar_empty(const MmaCtx& c, int s) {
+  return c.bar0 + 8u * (kStages + s);
+}
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The same barrier, and whether any of the 128 threads says so: every warp
+// takes the same way out.
+__device__ __forceinline__ bool compute_sync_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// One piece on the four compute warps: WM warps along the rows, WN along a
+// tile's keys.  false: a warp's wait gave up.
+template <int D, int WM, int WN>
+__device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kBN, kMaxRows>& k, MmaCtx& ctx) {
+  using C = MmaCfg<D>;
+  constexpr int kWarpKeys = kBN / WN;
+  constexpr int kSub = WN == 4 ? 16 : (D == 256 ? 16 : 32);  // keys of one softmax step
+  constexpr int kPairs = kSub / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp / WN, wn = warp % WN;
+  const int gh = k.group_heads;
+  const int h = k.seg / k.rt, rt = k.seg - h * k.rt;
+  const int rows = (k.it.t1 - k.it.t0) * gh;
+  const int row0 = rt * k.tm;  // first row of the tile
+  const float scale_log2 = w.scale * kLog2e;
+
+  // this thread's two rows: lane / 4 and + 8 of the warp's 16
+  int lim[2];
+  const __nv_bfloat16* qrow[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = row0 + wm * 16 + (lane >> 2) + 8 * e;
+    lim[e] = 0;
+    qrow[e] = nullptr;
+    if (r < rows) {
+      const int t = k.it.t0 + r / gh;
+      const int b = k.i < k.groups ? paged_seq_of(w.p, t) : k.it.row;
+      lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
+      qrow[e] = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride + static_cast<long long>(h * gh + r % gh) * D;
+    }
+  }
+  // the warp's smallest and largest limit over its valid rows
+  int lim_min = min(qrow[0] ? lim[0] : INT_MAX, qrow[1] ? lim[1] : INT_MAX), lim_max = max(lim[0], lim[1]);
+  lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+  lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+
+  uint32_t qf[D / 16][4];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat16* q = qrow[e & 1];
+      qf[s][e] = q == nullptr ? 0u : *reinterpret_cast<const uint32_t*>(q + 16 * s + (e >> 1) * 8 + (lane & 3) * 2);
+    }
+  }
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  const int krow = (lane & 7) + ((lane >> 4) << 3);        // K fragment rows: two 8-key groups
+  const int kchunk = (lane >> 3) & 1;
+  const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);  // V fragment rows (transposed): 16 keys
+  const int vchunk = lane >> 4;
+
+  bool ok = true;  // a warp whose wait gave up still takes part in the barriers below
+  for (int kt = 0; kt < k.count; ++kt) {
+    ok = mbar_wait(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag, w.status);
+    if (!ok) break;
+    const uint32_t sk = ctx.sbase + ctx.stage * 2 * C::kTileBytes, sv = sk + C::kTileBytes;
+    const int tile0 = (k.first + k.kt + kt) * kBN;
+    if (lim_max > 0) {
+#pragma unroll 1
+      for (int sub = 0; sub < kWarpKeys; sub += kSub) {
+        const int r0 = wn * kWarpKeys + sub;  // first key within the tile
+        const int key0 = tile0 + r0;
+        if (key0 >= lim_max || key0 + kSub <= k.it.lo) continue;
+        float s[kSub / 8][4];
+#pragma unroll
+        for (int j = 0; j < kSub / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+          for (int pr = 0; pr < kPairs; ++pr) {
+            const int row = r0 + pr * 16 + krow;
+            const int chunk = (ks & 3) * 2 + kchunk;
+            uint32_t b[4];
+            ldsm4(b, sk + (ks >> 2) * (kBN * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
+            mma_bf16(s[2 * pr], qf[ks], b[0], b[1]);
+            mma_bf16(s[2 * pr + 1], qf[ks], b[2], b[3]);
+          }
+        }
+        const bool edge = key0 < k.it.lo || key0 + kSub > lim_min;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < kSub / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 8 * j + 2 * (lane & 3) + (e & 1);
+              if (key < k.it.lo || key >= lim[e >> 1]) s[j][e] = -INFINITY;
+            }
+        }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < kSub / 8; ++j) {
+          mx[0] = fmax3(mx[0], s[j][0], s[j][1]);
+          mx[1] = fmax3(mx[1], s[j][2], s[j][3]);
+        }
+        bool grew = false;
+        float mnew[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+          mnew[e] = fmaxf(m[e], mx[e] * scale_log2);
+          grew |= mnew[e] > m[e];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            al[e] = mnew[e] > m[e] ? ex2_approx(m[e] - mnew[e]) : 1.f;
+            m[e] = mnew[e];
+            l[e] *= al[e];
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= al[0];
+            o[j][1] *= al[0];
+            o[j][2] *= al[1];
+            o[j][3] *= al[1];
+          }
+        }
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+        uint32_t pa[kPairs][4];
+#pragma unroll
+        for (int j = 0; j < kSub / 8; ++j) {
+          const float p0 = ex2_approx(fmaf(s[j][0], scale_log2, -mu[0]));
+          const float p1 = ex2_approx(fmaf(s[j][1], scale_log2, -mu[0]));
+          const float p2 = ex2_approx(fmaf(s[j][2], scale_log2, -mu[1]));
+          const float p3 = ex2_approx(fmaf(s[j][3], scale_log2, -mu[1]));
+          l[0] += p0 + p1;
+          l[1] += p2 + p3;
+          pa[j >> 1][(j & 1) * 2] = pack_f16(p0, p1);
+          pa[j >> 1][(j & 1) * 2 + 1] = pack_f16(p2, p3);
+        }
+#pragma unroll
+        for (int pr = 0; pr < kPairs; ++pr) {
+          // slots that hold no key of this item may hold anything, NaN
+          // included, and 0 * NaN is NaN: such V rows are taken as zero
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + pr * 16 + e * 8 + 2 * (lane & 3);
+              keep[e] = (key >= k.it.lo && key < k.it.hi ? 0xffffu : 0u) |
+                        (key + 1 >= k.it.lo && key + 1 < k.it.hi ? 0xffff0000u : 0u);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const int row = r0 + pr * 16 + vrow;
+            const int chunk = (j & 3) * 2 + vchunk;
+            uint32_t b[4];
+            ldsm4_t(b, sv + (j >> 2) * (kBN * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
+            mma_f16(o[2 * j], pa[pr], b[0] & keep[0], b[1] & keep[1]);
+            mma_f16(o[2 * j + 1], pa[pr], b[2] & keep[0], b[3] & keep[1]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty<C::kStages>(ctx, ctx.stage));
+    if (++ctx.stage == C::kStages) {
+      ctx.stage = 0;
+      ctx.phase ^= 1u;
+    }
+  }
+
+  // join the WN warps of each row group, a quarter of the columns at a time,
+  // in the order of the warps
+  float* join = reinterpret_cast<float*>(ctx.smem + C::kOffJoin);
+  float2* ml = reinterpret_cast<float2*>(ctx.smem + C::kOffMl);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    if ((lane & 3) == 0) ml[warp * 16 + (lane >> 2) + 8 * e] = make_float2(m[e], l[e]);
+  }
+  compute_sync();
+  float f[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
+    f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
+  }
+  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg, k.tm);
+  const int valid = min(rows - row0, WM * 16);
+  if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
+    const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(g * WN + x) * 16 + r].x);
+#pragma unroll
+    for (int x = 0; x < WN; ++x) {
+      const float2 v = ml[(g * WN + x) * 16 + r];
+      sum += v.y * (top == -INFINITY ? 1.f : ex2_approx(v.x - top));
+    }
+    w.part_ml[part + threadIdx.x] = make_float2(top, sum);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const int jj = c * (D / 32) + j;
+      float* dst = join + (warp * 16 + (lane >> 2)) * C::kJoinStride + 8 * j + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(dst) = make_float2(o[jj][0] * f[0], o[jj][1] * f[0]);
+      *reinterpret_cast<float2*>(dst + 8 * C::kJoinStride) = make_float2(o[jj][2] * f[1], o[jj][3] * f[1]);
+    }
+    compute_sync();
+    constexpr int kVecs = D / 16;  // float4s of a row's quarter
+    for (int x = threadIdx.x; x < valid * kVecs; x += 128) {
+      const int r = x / kVecs, v = x % kVecs;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < WN; ++y) {
+        const float4 u = *reinterpret_cast<const float4*>(
+            join + (((r >> 4) * WN + y) * 16 + (r & 15)) * C::kJoinStride + 4 * v);
+        a.x += u.x;
+        a.y += u.y;
+        a.z += u.z;
+        a.w += u.w;
+      }
+      *reinterpret_cast<float4*>(w.part_o + (part + r) * D + c * (D / 4) + 4 * v) = a;
+    }
+    if (c < 3) compute_sync();
+  }
+  return !compute_sync_or(!ok);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
+    paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ PagedWork w, int groups) {
+  using C = MmaCfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  MmaCtx ctx;
+  ctx.smem = smem;
+  ctx.sbase = smem_u32(smem);
+  ctx.bar0 = ctx.sbase + C::kOffBar;
+  ctx.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * 2 * C::kStages);
+  ctx.stage = 0;
+  ctx.phase = 0;
+  PagedScan* sc = reinterpret_cast<PagedScan*>(smem + C::kOffScan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_full(ctx, s), 1);
+      mbar_init(bar_empty<C::kStages>(ctx, s), 4);
+    }
+    *ctx.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kProducer && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, groups, w.items, sc, w.status);  // syncs the CTA
+
+  PagedWalk<kBN, kMaxRows> walk;
+  if (!walk.init(&w.p, gh, groups, sc)) return;  // uniform for the CTA
+
+  if (warp == kProducer) {
+    // a lane for each box of a tile: (page part, 64-column slice, K or V)
+    const int ps = w.p.page_size;
+    const int box = ps < kBN ? ps : kBN;
+    const int kv = lane & 1, sl = (lane >> 1) % C::kSlices, pp = (lane >> 1) / C::kSlices;
+    const bool mine = pp < kBN / box;
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
+    const uint32_t dst0 = ctx.sbase + kv * C::kTileBytes + sl * (kBN * 128) + pp * box * 128;
+    int issued = 0;
+    bool ok = true;
+    do {
+      const int h = walk.seg / walk.rt;
+      const int* table = w.p.block_table + static_cast<long long>(walk.it.row) * w.p.table_stride;
+      // the page of this lane's part of a tile, -1 where the item has no key in it
+      auto page_at = [&](int kt) -> int {
+        const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
+        if (kt >= walk.count || !mine || key >= walk.it.hi || key + box <= walk.it.lo) return -1;
+        const int pg = table[key / ps];
+        if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) return pg;
+        report(w.status, kDevCheck);
+        return w.p.num_pages;  // outside the map: the box arrives as zeros
+      };
+      int page = page_at(0);
+      for (int kt = 0; kt < walk.count; ++kt) {
+        const int page_next = page_at(kt + 1);
+        const int s = ctx.stage;
+        if (issued >= C::kStages) ok = mbar_wait(bar_empty<C::kStages>(ctx, s), ctx.phase ^ 1u, ctx.abort_flag, w.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned active = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(bar_full(ctx, s), __popc(active) * box * 128);
+        __syncwarp();
+        if (page >= 0) {
+          const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
+          tma_load_4d(dst0 + s * 2 * C::kTileBytes, map, bar_full(ctx, s), sl * 64, key % ps, h, page);
+        }
+        ++issued;
+        page = page_next;
+        if (++ctx.stage == C::kStages) {
+          ctx.stage = 0;
+          ctx.phase ^= 1u;
+        }
+      }
+    } while (ok && walk.next());
+    if (*ctx.abort_flag && lane == 0) {
+      // let copies already in flight land before the CTA exits (bounded)
+      volatile int never = 0;
+      for (int x = max(0, issued - C::kStages); x < issued; ++x)
+        mbar_wait(bar_full(ctx, x % C::kStages), (x / C::kStages) & 1, &never, nullptr, 10000000ull);
+    }
+  } else {
+    bool ok;
+    do {
+      if (walk.tm == 16) {
+        ok = mma_piece<D, 1, 4>(w, walk, ctx);
+      } else if (walk.tm == 32) {
+        ok = mma_piece<D, 2, 2>(w, walk, ctx);
+      } else {
+        ok = mma_piece<D, 4, 1>(w, walk, ctx);
+      }
+    } while (ok && walk.next());
+  }
+}
+
+// ------------------------------------------------------------------ fp32
+constexpr int kFBN = 32;    // keys a tile
+constexpr int kFRows = 16;  // rows a tile
+constexpr int kFThreads = 128;
+
+template <int D>
+struct F32Cfg {
+  static constexpr int kStride = D + 4;  // floats; + 4: 16-byte reads of consecutive rows hit all banks
+  static constexpr int kTile = kFBN * kStride;
+  static constexpr int kOffQ = 2 * 2 * kTile * 4;
+  static constexpr int kOffP = kOffQ + kFRows * D * 4;
+  static constexpr int kOffScan = kOffP + kFBN * kFRows * 4;
+  static constexpr int kSmemBytes = kOffScan + static_cast<int>(sizeof(PagedScan));
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;  // 0: the destination is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFThreads)
+    paged_f32_kernel(const __grid_constant__ PagedWork w, int groups) {
+  using C = F32Cfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  float* kv = reinterpret_cast<float*>(smem_raw);
+  float* qs = reinterpret_cast<float*>(smem_raw + C::kOffQ);  // [row][D]
+  float* ps = reinterpret_cast<float*>(smem_raw + C::kOffP);  // [warp][key][4 rows]
+  PagedScan* sc = reinterpret_cast<PagedScan*>(smem_raw + C::kOffScan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, groups, w.items, sc, w.status);
+  PagedWalk<kFBN, kFRows> k;
+  if (!k.init(&w.p, gh, groups, sc)) return;
+  const float scale_log2 = w.scale * kLog2e;
+  do {
+    const int h = k.seg / k.rt, rt = k.seg - h * k.rt;
+    const int rows = (k.it.t1 - k.it.t0) * gh, row0 = rt * k.tm;
+    const int* table = w.p.block_table + static_cast<long long>(k.it.row) * w.p.table_stride;
+    auto fetch = [&](int kt) {
+      const int buf = kt & 1;
+      const int tile0 = (k.first + k.kt + kt) * kFBN;
+      for (int x = threadIdx.x; x < kFBN * (D / 4); x += kFThreads) {
+        const int r = x / (D / 4), c = x % (D / 4);
+        const int key = tile0 + r;
+        bool take = key >= k.it.lo && key < k.it.hi;
+        long long off = 0;
+        if (take) {
+          const int pg = table[key / w.p.page_size];
+          if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) {
+            off = pg * w.p.page_stride + (static_cast<long long>(h) * w.p.page_size + key % w.p.page_size) * D + 4 * c;
+          } else {
+            take = false;  // taken as zeros
+            report(w.status, kDevCheck);
+          }
+        }
+        const uint32_t dst = smem_u32(kv + (buf * 2) * C::kTile + r * C::kStride + 4 * c);
+        cp_async16(dst, static_cast<const float*>(w.p.k_pages) + off, take);
+        cp_async16(dst + C::kTile * 4, static_cast<const float*>(w.p.v_pages) + off, take);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncthreads();  // the previous piece is read out
+    fetch(0);
+    for (int x = threadIdx.x; x < kFRows * (D / 4); x += kFThreads) {
+      const int r = row0 + x / (D / 4), c = x % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        const int t = k.it.t0 + r / gh;
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(w.q) + t * w.q_stride +
+                                             static_cast<long long>(h * gh + r % gh) * D + 4 * c);
+      }
+      *reinterpret_cast<float4*>(qs + (x / (D / 4)) * D + 4 * c) = v;
+    }
+    // warp w has rows 4w .. 4w + 3
+    int lim[4];
+    float m[4], l[4];
+    constexpr int kCols = D / 32;  // columns of a lane
+    float o[4][kCols];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = row0 + warp * 4 + e;
+      lim[e] = 0;
+      if (r < rows) {
+        const int t = k.it.t0 + r / gh;
+        const int b = k.i < groups ? paged_seq_of(w.p, t) : k.it.row;
+        lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
+      }
+      m[e] = -INFINITY;
+      l[e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[e][c] = 0.f;
+    }
+    for (int kt = 0; kt < k.count; ++kt) {
+      if (kt + 1 < k.count) {
+        fetch(kt + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      __syncthreads();
+      const float* ks = kv + (kt & 1) * 2 * C::kTile;
+      const float* vs = ks + C::kTile;
+      const int key = (k.first + k.kt + kt) * kFBN + lane;  // a lane has one key
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int c = 0; c < D; c += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(ks + lane * C::kStride + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 b = *reinterpret_cast<const float4*>(qs + (warp * 4 + e) * D + c);
+          s[e] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[e]))));
+        }
+      }
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = key < k.it.lo || key >= lim[e] ? -INFINITY : s[e] * scale_log2;
+        float mx = x;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mn = fmaxf(m[e], mx);
+        const float al = mn > m[e] ? ex2_approx(m[e] - mn) : 1.f;
+        m[e] = mn;
+        p[e] = ex2_approx(x - (mn == -INFINITY ? 0.f : mn));
+        l[e] = l[e] * al + p[e];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[e][c] *= al;
+      }
+      *reinterpret_cast<float4*>(ps + (warp * kFBN + lane) * 4) = make_float4(p[0], p[1], p[2], p[3]);
+      __syncwarp();
+#pragma unroll 4
+      for (int j = 0; j < kFBN; ++j) {
+        const float4 pj = *reinterpret_cast<const float4*>(ps + (warp * kFBN + j) * 4);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float v = vs[j * C::kStride + c * 32 + lane];
+          o[0][c] = fmaf(pj.x, v, o[0][c]);
+          o[1][c] = fmaf(pj.y, v, o[1][c]);
+          o[2][c] = fmaf(pj.z, v, o[2][c]);
+          o[3][c] = fmaf(pj.w, v, o[3][c]);
+        }
+      }
+      __syncthreads();  // the buffer is free for the tile after next
+    }
+    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg, k.tm);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float sum = l[e];
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const int r = warp * 4 + e;
+      if (row0 + r < rows) {
+        if (lane == 0) w.part_ml[part + r] = make_float2(m[e], sum);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) w.part_o[(part + r) * D + c * 32 + lane] = o[e][c];
+      }
+    }
+  } while (k.next());
+}
+
+// ------------------------------------------------------------------ join
+// One CTA for each (token, head): the partials of the row's prefix segment and
+// of its own segment, in the order of the CTAs that made them.
+template <int D, typename T, int BN, int kMax>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w, int groups, int ctas) {
+  constexpr int kCols = D / 32;
+  const int t = blockIdx.x, h = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  const int b = paged_seq_of(w.p, t);
+  T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
+  if (paged_limit(w.p, b, t) <= 0) {
+    for (int c = threadIdx.x; c < D; c += 128) out[c] = static_cast<T>(0.f);
+    if (w.lse != nullptr && threadIdx.x == 0) w.lse[static_cast<long long>(t) * w.num_q_heads + h] = -INFINITY;
+    return;
+  }
+  const int n = groups + w.p.num_seqs;
+  const long long total = w.items[n];
+  // the row's two segments: partial rows part[x] + j * kMax for j < count[x]
+  long long part[2];
+  int count[2] = {0, 0};
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    part[x] = 0;
+    if (x == 0 && groups == 0) continue;
+    const int i = x == 0 ? paged_group_of(w.p, b) : groups + b;
+    const PagedItem it = paged_item(w.p, i, groups);
+    const PagedSpan<BN, kMax> sp(it, gh);
+    if (sp.nt == 0) continue;
+    const int r = (t - it.t0) * gh + h % gh;
+    const int seg = (h / gh) * sp.rt + r / sp.tm;
+    const long long u0 = w.items[i] + static_cast<long long>(seg) * sp.nt;
+    const int c0 = paged_owner(u0, total, ctas), c1 = paged_owner(u0 + sp.nt - 1, total, ctas);
+    part[x] = paged_part_row(c0, kMax, w.items[n + 1 + i], seg, sp.tm) + r % sp.tm;
+    count[x] = c1 - c0 + 1;
+  }
+  const int all = count[0] + count[1];
+  auto row_of = [&](int j) -> long long {
+    return j < count[0] ? part[0] + static_cast<long long>(j) * kMax
+                        : part[1] + static_cast<long long>(j - count[0]) * kMax;
+  };
+  __shared__ float red[4];
+  __shared__ float acc_s[4][D + 1];
+  float top = -INFINITY;
+  for (int j = threadIdx.x; j < all; j += 128) top = fmaxf(top, w.part_ml[row_of(j)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float base = top == -INFINITY ? 0.f : top;
+  float acc[kCols], sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int j = warp; j < all; j += 4) {
+    const long long r = row_of(j);
+    const float2 v = w.part_ml[r];
+    const float f = ex2_approx(v.x - base);
+    sum += v.y * f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(w.part_o[r * D + c * 32 + lane], f, acc[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
+  if (lane == 0) acc_s[warp][D] = sum;
+  __syncthreads();
+  const float l = (acc_s[0][D] + acc_s[1][D]) + (acc_s[2][D] + acc_s[3][D]);
+  const float inv = 1.f / l;
+  for (int c = threadIdx.x; c < D; c += 128)
+    out[c] = static_cast<T>(((acc_s[0][c] + acc_s[1][c]) + (acc_s[2][c] + acc_s[3][c])) * inv);
+  if (w.lse != nullptr && threadIdx.x == 0)
+    w.lse[static_cast<long long>(t) * w.num_q_heads + h] = (top + log2f(l)) * kLn2;
+}
+
+// (d, page_size, Hkv, pages) view of a 16-bit page array; one box is 64 columns
+// of up to 64 tokens of a page, rows of 128 bytes, swizzled.
+CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, bool f16) {
+  const TensorMapEncodeFn fn = tensor_map_encode_fn();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.page_size),
+                              static_cast<cuuint64_t>(p.num_kv_heads), static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.head_dim) * 2,
+                                 static_cast<cuuint64_t>(p.page_size) * p.head_dim * 2,
+                                 static_cast<cuuint64_t>(p.page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page_size < kBN ? p.page_size : kBN), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// CTAs of the grid at most: what the partials are sized for.
+constexpr int kMaxCtas = 148 * 3;
+
+template <int D, typename T, int BN, int kMax>
+cudaError_t join(const PagedWork& w, int groups, int ctas, cudaStream_t stream) {
+  paged_join_kernel<D, T, BN, kMax><<<dim3(w.p.total_q, w.num_q_heads), 128, 0, stream>>>(w, groups, ctas);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_mma(const PagedWork& w, int groups, cudaStream_t stream) {
+  using C = MmaCfg<D>;
+  CUtensorMap mk, mv;
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, false) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, true) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int ctas = sm_count() * C::kCtas < kMaxCtas ? sm_count() * C::kCtas : kMaxCtas;
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  paged_mma_kernel<D><<<ctas, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w, groups);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return join<D, __nv_bfloat16, kBN, kMaxRows>(w, groups, ctas, stream);
+}
+
+template <int D>
+cudaError_t run_f32(const PagedWork& w, int groups, cudaStream_t stream) {
+  using C = F32Cfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int per_sm = D == 256 ? 1 : D == 128 ? 2 : 3;
+  const int ctas = sm_count() * per_sm < kMaxCtas ? sm_count() * per_sm : kMaxCtas;
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  paged_f32_kernel<D><<<ctas, kFThreads, C::kSmemBytes, stream>>>(w, groups);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return join<D, float, kFBN, kFRows>(w, groups, ctas, stream);
+}
+
+}  // namespace
+
+PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group_ptr, int num_q_heads, int dtype) {
+  PagedShape s;
+  s.num_items = p.num_groups + p.num_seqs;
+  const int gh = num_q_heads / p.num_kv_heads;
+  const int max_rows = dtype == DHSA_BF16 ? kMaxRows : kFRows;
+  long long rows = 0;
+  auto add = [&](long long r) {
+    const int tm = dtype == DHSA_BF16 ? paged_tile_rows<kMaxRows>(static_cast<int>(r))
+                                      : paged_tile_rows<kFRows>(static_cast<int>(r));
+    rows += (r + tm - 1) / tm * tm;
+  };
+  for (int g = 0; g < p.num_groups; ++g)
+    add(static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh);
+  for (int b = 0; b < p.num_seqs; ++b) add(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);
+  s.part_rows = rows * p.num_kv_heads + static_cast<long long>(kMaxCtas) * max_rows;
+  return s;
+}
+
+cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream) {
+  (void)shape;
+  if (w.p.total_q <= 0) return cudaSuccess;
+  const int groups = w.p.num_groups;
+  if (dtype == DHSA_BF16) {
+    switch (w.p.head_dim) {
+      case 64: return run_mma<64>(w, groups, stream);
+      case 128: return run_mma<128>(w, groups, stream);
+      default: return run_mma<256>(w, groups, stream);
+    }
+  }
+  switch (w.p.head_dim) {
+    case 64: return run_f32<64>(w, groups, stream);
+    case 128: return run_f32<128>(w, groups, stream);
+    default: return run_f32<256>(w, groups, stream);
+  }
+}
+
+}  // namespace dhsa

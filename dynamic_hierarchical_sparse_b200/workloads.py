@@ -86,6 +86,22 @@ class SegmentRule:
 
 
 @dataclasses.dataclass(frozen=True)
+class RopeScaling:
+    """How rotary frequencies are stretched for contexts beyond the original
+    length: ``linear`` (factor), ``llama3`` (factor, original_len,
+    low_freq_factor, high_freq_factor) or ``yarn`` (factor, original_len,
+    beta_fast, beta_slow)."""
+
+    kind: str
+    factor: float
+    original_len: float = 0.0
+    low_freq_factor: float = 1.0
+    high_freq_factor: float = 4.0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+
+
+@dataclasses.dataclass(frozen=True)
 class WorkloadSpec:
     name: str
     seq_lens: Sequence[int]

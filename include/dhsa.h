@@ -340,6 +340,184 @@ DHSA_API dhsa_status dhsa_plan_noalloc(const void* q, const void* k, const dhsa_
                                        dhsa_budget budget, int32_t* row_ptr, int32_t* col,
                                        int64_t nnz, void* stream);
 
+/* ======================= around the prefill path ===========================
+ * The path above takes rotated queries and keys and returns the prompt's
+ * attention output.  The three operators below stand before and behind it:
+ * rotary positions of packed q and k, storing keys and values in a paged cache
+ * (the rotation applied on the way), and attention of new query tokens over
+ * that cache, where sequences that share a long prefix read it once for all.
+ * The pages have no counterpart of them: they are interface additions for
+ * callers that prefill with this library and go on to answer.
+ *
+ * The status word of these calls is not cleared by them: it gathers the
+ * reports of every call since the caller last zeroed the first 256 bytes of
+ * the workspace (once, before the first call), so that a captured decode loop
+ * can be checked after many steps.  dhsa_workspace_status reads it. */
+
+/* A packed [T, H, d] tensor whose tokens may lie apart (a slice of a fused
+ * projection's output): the H * d elements of one token are contiguous, token
+ * t starts at data + t * token_stride elements.  token_stride 0 stands for
+ * H * d.  data 16-byte aligned, token_stride a multiple of 16 bytes.  An
+ * optional tensor that is left out has data NULL. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+} dhsa_tokens;
+
+/* ---- rotary positions -----------------------------------------------------
+ * The first rotary_dim of a head's d numbers form rotary_dim / 2 pairs; pair i
+ * of a token at position p turns by the angle p * f_i,
+ *     y1 = a (x1 cos - x2 sin),   y2 = a (x2 cos + x1 sin),
+ * the numbers behind rotary_dim stay as they are.  Pairs are (i, i +
+ * rotary_dim / 2), or (2i, 2i + 1) when interleaved.  f_i = base^(-2i /
+ * rotary_dim), stretched for long contexts by one of
+ *   LINEAR  f_i / factor;
+ *   LLAMA3  with r = original_len f_i / (2 pi) turns in the original length:
+ *           f_i above high_freq_factor turns, f_i / factor below
+ *           low_freq_factor, between them the mix that is linear in r;
+ *   YARN    f_i / factor * w + f_i * (1 - w), w rising linearly from 0 to 1
+ *           between the pair indexes that make beta_fast and beta_slow turns in
+ *           original_len (rounded down and up, kept within 0 .. rotary_dim - 1),
+ *           and a = 0.1 ln(factor) + 1; otherwise a = 1.
+ * Angles are exact for every position: the table holds f_i / (2 pi) as a
+ * 64-bit binary fraction of a turn, and position times fraction is integer
+ * arithmetic modulo one turn (error 2^-32 turns from the top 32 bits, plus
+ * |p| 2^-64).  cos, sin and the rotation are fp32, each output rounded once. */
+#define DHSA_ROPE_MAX_PAIRS 128
+typedef enum {
+  DHSA_ROPE_UNSCALED = 0,
+  DHSA_ROPE_LINEAR = 1,
+  DHSA_ROPE_LLAMA3 = 2,
+  DHSA_ROPE_YARN = 3
+} dhsa_rope_kind;
+typedef struct {
+  int32_t kind;            /* dhsa_rope_kind */
+  double factor;           /* >= 1 (kinds other than UNSCALED) */
+  double original_len;     /* > 0 (LLAMA3, YARN) */
+  double low_freq_factor;  /* LLAMA3: 0 < low < high */
+  double high_freq_factor;
+  double beta_fast;        /* YARN: beta_fast >= beta_slow > 0 */
+  double beta_slow;
+} dhsa_rope_scaling;
+/* Host data, filled by dhsa_rope_init or dhsa_rope_init_freq and read during a
+ * call only (a captured call keeps the values it was captured with). */
+typedef struct {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float factor;                            /* a */
+  uint64_t turns[DHSA_ROPE_MAX_PAIRS];     /* f_i / (2 pi) modulo 1, times 2^64 */
+} dhsa_rope_table;
+
+/* Host only.  rotary_dim even, 2 .. 256; base > 1; scaling NULL or checked as
+ * above. */
+DHSA_API dhsa_status dhsa_rope_init(dhsa_rope_table* rope, int32_t rotary_dim, int32_t interleaved, double base,
+                                    const dhsa_rope_scaling* scaling);
+/* Host only: the caller's own frequencies inv_freq[rotary_dim / 2] (radians a
+ * position, finite) and factor a (finite). */
+DHSA_API dhsa_status dhsa_rope_init_freq(dhsa_rope_table* rope, int32_t rotary_dim, int32_t interleaved,
+                                         const double* inv_freq, double factor);
+/* Rotates q [T, Hq, d] and k [T, Hkv, d] (either may be left out) in one
+ * launch.  positions device int32 [T], any value.  An output may be its own
+ * input (same data and token_stride); any other overlap of an output with an
+ * input or output is refused.  dtype bf16 or fp32, d in {64, 128, 256},
+ * rotary_dim <= d. */
+DHSA_API dhsa_status dhsa_rope(const dhsa_rope_table* rope, int32_t dtype, int32_t head_dim, int32_t total_tokens,
+                               const int32_t* positions, dhsa_tokens q, int32_t num_q_heads, dhsa_tokens q_out,
+                               dhsa_tokens k, int32_t num_kv_heads, dhsa_tokens k_out, void* stream);
+
+/* ---- paged cache ----------------------------------------------------------
+ * Keys and values of many sequences in pages of page_size tokens.  A page
+ * holds [Hkv, page_size, d], contiguous; page p starts at p * page_stride
+ * elements.  K pages are of `dtype`; V pages are f16 for bf16 problems (the
+ * products of attention take P and V in f16, see dhsa_attention: a bf16 value
+ * is exact in f16 for magnitudes from 2^-14 to 65504 and below that rounds by
+ * at most 2^-25) and fp32 for fp32 ones. */
+typedef struct {
+  int32_t dtype;         /* dhsa_dtype */
+  int32_t num_kv_heads;  /* Hkv >= 1 */
+  int32_t head_dim;      /* d in {64, 128, 256} */
+  int32_t page_size;     /* tokens a page: 16, 32, 64 or 128 */
+  int32_t num_pages;     /* >= 1 */
+  int64_t page_stride;   /* elements from page to page: >= Hkv * page_size * d, a multiple of 16 bytes */
+  void* k_pages;         /* device, 16-byte aligned */
+  void* v_pages;
+} dhsa_paged_cache;
+
+/* One step of a batch: sequence b brings the tokens cu_q[b] .. cu_q[b+1]-1
+ * (n_b >= 0 of them) of the packed tensors and holds kv_lens[b] tokens with
+ * them, so its new token j is at position kv_lens[b] - n_b + j.  Token s of the
+ * sequence is in slot s % page_size of page block_table[b * table_stride + s /
+ * page_size].  Tokens at negative positions (kv_lens[b] < n_b, down to 0 for a
+ * slot of the batch that is idle) are padding: not stored, their attention 0.
+ * Rows of the packed tensors from cu_q[B] on are padding: they are
+ * neither read nor written.
+ * Groups: the sequences group_ptr[g] .. group_ptr[g+1]-1 (every sequence in
+ * exactly one group) share their first prefix_lens[g] tokens, which are read
+ * through the table row of the group's first sequence; they have to be stored
+ * there, also where kv_lens is shorter.  A prefix may end inside a page.
+ * num_groups 0 (the three group pointers NULL): nothing is shared.
+ * kv_lens, block_table and prefix_lens are read on the device by every call, so
+ * a captured call follows their new contents; what is wrong in them (lengths
+ * and prefix lengths outside 0 .. max_pages * page_size, pages outside the cache;
+ * the prefix of a group without new tokens is not looked at) is reported as DHSA_ERR_DEVICE_CHECK, and
+ * nothing outside the cache is touched. */
+typedef struct {
+  int32_t num_seqs;             /* B >= 0 */
+  int32_t max_pages;            /* entries of a block_table row, >= 1; max_pages * page_size <= 2^30 */
+  int32_t table_stride;         /* >= max_pages */
+  int32_t num_groups;           /* G >= 0 */
+  const int32_t* cu_q;          /* device [B+1] */
+  const int32_t* kv_lens;       /* device [B] */
+  const int32_t* block_table;   /* device [B, table_stride] */
+  const int32_t* group_ptr;     /* device [G+1] */
+  const int32_t* prefix_lens;   /* device [G] */
+  const int32_t* h_cu_q;        /* host mirror [B+1] */
+  const int32_t* h_group_ptr;   /* host mirror [G+1] */
+} dhsa_paged_batch;
+
+/* Stores the new tokens' keys and values, in one launch:
+ *   K page slot of the token = k, rotated at the token's position (by
+ *     positions[t] instead where `positions`, device int32 [cu_q[B]], is given;
+ *     not rotated when rope is NULL);
+ *   V page slot = v (bf16 problems: in f16; larger magnitudes than 65504 are
+ *     stored as +-65504, NaN as NaN, and both are reported as
+ *     DHSA_ERR_DEVICE_CHECK);
+ *   k_out = the rotated k, packed (optional; for dhsa_plan / dhsa_attention);
+ *   q_out = q rotated likewise (optional, q and q_out together; needs rope).
+ * q, k, v and the outputs are packed tensors of cu_q[B] tokens or more; k_out
+ * may be k and q_out may be q.  A token whose position is beyond the table or
+ * whose page is outside the cache is reported and not stored (its q_out and
+ * k_out are written all the same, as a padding token's are).  No page
+ * slot may belong to two of the call's tokens.  Groups are not read.
+ *   workspace  device, >= 256 bytes: the status word (see above) */
+DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_paged_batch* batch,
+                                    const dhsa_rope_table* rope, const int32_t* positions, dhsa_tokens k,
+                                    dhsa_tokens v, dhsa_tokens k_out, dhsa_tokens q, dhsa_tokens q_out,
+                                    int32_t num_q_heads, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Causal attention of the new tokens over the cache: with L = kv_lens[b] - n_b
+ * + j + 1 tokens visible to token j of sequence b,
+ *   out[t, h] = sum over s < L of softmax_s(q[t, h] . k[s, g] * scale) v[s, g],
+ *   lse[t, h] = ln of the sum of exp(q[t, h] . k[s, g] * scale),  g = h / (Hq / Hkv).
+ * One token a sequence is a decode step; several are drafted tokens, or a
+ * prompt's next part.  A group's prefix is read once for all its sequences.
+ * L <= 0: out is 0 and lse -infinity.  scale <= 0 selects 1 / sqrt(d).  fp32
+ * accumulation and softmax; bf16 problems take the weights in f16 (as
+ * dhsa_attention).  A NaN or an infinity in a stored value (V) at a position
+ * below a sequence's kv_lens, or in a shared prefix, may reach all the query
+ * rows that are worked on together, also those to which the position is not
+ * visible; keys (K), and slots at or behind kv_lens, reach no row that does not
+ * see them.  Results are the same from call to call.
+ *   q, out     [T, Hq, d] in the cache's dtype; must not overlap
+ *   lse        device fp32 [T, Hq] contiguous, or NULL
+ *   workspace  dhsa_paged_attention_workspace_size bytes, 256-byte aligned; a
+ *              workspace serves one call at a time */
+DHSA_API dhsa_status dhsa_paged_attention_workspace_size(const dhsa_paged_cache* cache, const dhsa_paged_batch* batch,
+                                                         int32_t num_q_heads, size_t* bytes);
+DHSA_API dhsa_status dhsa_paged_attention(const dhsa_paged_cache* cache, const dhsa_paged_batch* batch, dhsa_tokens q,
+                                          int32_t num_q_heads, float scale, dhsa_tokens out, float* lse,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
