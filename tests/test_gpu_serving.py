@@ -47,6 +47,8 @@ ROPE_CASES = [
     (2049, 8, 4, 256, 64, True, YARN, 10000.0, F32),
     (3000, 32, 8, 128, 128, False, LLAMA3, 500000.0, F32),
     (40, 5, 5, 128, 30, False, None, 10000.0, F32),
+    (55, 7, 3, 128, 100, False, None, 10000.0, BF16),   # vectors of 4 bytes
+    (55, 7, 3, 256, 36, True, None, 10000.0, F32),      # vectors of 8 bytes
 ]
 
 
