@@ -121,7 +121,7 @@ PagedArgs paged_args(const dhsa_paged_cache* c, const dhsa_paged_batch* b) {
 
 struct AttentionLayout {
   PagedShape shape;
-  size_t items, ml, o, total;
+  size_t items[2], ml[2], o[2], total;  // of the prefixes' own list and of the other
 };
 
 dhsa_status attention_layout(const dhsa_paged_cache* c, const dhsa_paged_batch* b, int num_q_heads,
@@ -130,10 +130,18 @@ dhsa_status attention_layout(const dhsa_paged_cache* c, const dhsa_paged_batch* 
   if (num_q_heads > 65535) return DHSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(a.total_q) * num_q_heads > INT32_MAX) return DHSA_ERR_UNSUPPORTED;
   L->shape = paged_shape(a, b->h_cu_q, b->h_group_ptr, num_q_heads, c->dtype);
-  L->items = kStatusBytes;
-  L->ml = L->items + align_up((2 * static_cast<size_t>(L->shape.num_items) + 1) * sizeof(long long));
-  L->o = L->ml + align_up(static_cast<size_t>(L->shape.part_rows) * sizeof(float2));
-  L->total = L->o + align_up(static_cast<size_t>(L->shape.part_rows) * c->head_dim * sizeof(float));
+  size_t at = kStatusBytes;
+  for (int x = 0; x < 2; ++x) {
+    const size_t rows = static_cast<size_t>(x == 0 ? L->shape.prefix_rows : L->shape.list_rows);
+    const size_t n = static_cast<size_t>(x == 0 ? L->shape.prefix_items : L->shape.list_items);
+    L->items[x] = at;
+    at += align_up((2 * n + 1) * sizeof(long long));
+    L->ml[x] = at;
+    at += align_up(rows * sizeof(float2));
+    L->o[x] = at;
+    at += align_up(rows * c->head_dim * sizeof(float));
+  }
+  L->total = at;
   return DHSA_OK;
 }
 
@@ -313,10 +321,18 @@ dhsa_status dhsa_paged_attention(const dhsa_paged_cache* cache, const dhsa_paged
   w.num_q_heads = num_q_heads;
   w.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
   w.status = reinterpret_cast<uint32_t*>(ws);
-  w.items = reinterpret_cast<long long*>(ws + L.items);
-  w.part_ml = reinterpret_cast<float2*>(ws + L.ml);
-  w.part_o = reinterpret_cast<float*>(ws + L.o);
-  return cuda_status(launch_paged_attention(w, L.shape, cache->dtype, static_cast<cudaStream_t>(stream)));
+  const int groups = w.p.num_groups;
+  w.prefix.begin = 0;
+  w.prefix.end = L.shape.own_prefix ? groups : 0;
+  w.list.begin = w.prefix.end;
+  w.list.end = groups + w.p.num_seqs;
+  for (int x = 0; x < 2; ++x) {
+    PagedList& l = x == 0 ? w.prefix : w.list;
+    l.items = reinterpret_cast<long long*>(ws + L.items[x]);
+    l.part_ml = reinterpret_cast<float2*>(ws + L.ml[x]);
+    l.part_o = reinterpret_cast<float*>(ws + L.o[x]);
+  }
+  return cuda_status(launch_paged_attention(w, cache->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -7,6 +7,18 @@
 
 namespace dhsa {
 
+// 4-D tiled load (no multicast) into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 // One item: the query tokens [t0, t1) over the keys [lo, hi) of a table row.
 struct PagedItem {
   int t0, t1, lo, hi, row;
@@ -42,11 +54,11 @@ __device__ __forceinline__ int paged_limit(const PagedArgs& p, int b, int t) {
   return paged_clamp_len(p, p.kv_lens[b]) - (p.cu_q[b + 1] - 1 - t);
 }
 
-// Item i: the groups come first, then the sequences.  `groups`: num_groups, or
-// 0 where the caller's list holds the sequences alone.
-__device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, int i, int groups) {
+// Item i: the groups come first, then the sequences.  A kernel's list is the
+// items begin .. end - 1 of them.
+__device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, int i) {
   PagedItem it;
-  if (i < groups) {
+  if (i < p.num_groups) {
     const int s0 = min(max(p.group_ptr[i], 0), p.num_seqs), s1 = min(max(p.group_ptr[i + 1], s0), p.num_seqs);
     it.t0 = p.cu_q[s0];
     it.t1 = p.cu_q[s1];
@@ -55,7 +67,7 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, int i, int g
     it.row = s0;
     if (s0 == s1) it.hi = 0;
   } else {
-    const int b = i - groups;
+    const int b = i - p.num_groups;
     it.t0 = p.cu_q[b];
     it.t1 = p.cu_q[b + 1];
     it.hi = paged_clamp_len(p, p.kv_lens[b]);
@@ -78,7 +90,9 @@ __host__ __device__ __forceinline__ int paged_tile_rows(int rows) {
 // An item's segments and key tiles.
 template <int BN, int kMaxRows>
 struct PagedSpan {
+  static constexpr int kMax = kMaxRows;
   int rows, tm, rt, first, nt;  // rows; rows a tile, row tiles; first key tile, key tiles
+  PagedSpan() = default;
   __device__ __forceinline__ PagedSpan(const PagedItem& it, int group_heads) {
     rows = (it.t1 - it.t0) * group_heads;
     tm = paged_tile_rows<kMaxRows>(rows);
@@ -126,23 +140,24 @@ struct PagedScan {
 // the item that holds its first unit.  CTA 0 writes the items' first units and
 // rows for the merge.  kThreads threads, all of them call this.
 template <int BN, int kMaxRows, int kThreads>
-__device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_heads, int groups, long long* items,
+__device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_heads, const PagedList& list,
                                                PagedScan* sc, uint32_t* status) {
-  const int n = groups + p.num_seqs;
+  const int n = list.end - list.begin;
   const int per = (n + kThreads - 1) / kThreads;
   const int i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
   long long units = 0, rows = 0;
   bool bad = false;
   for (int i = i0; i < i1; ++i) {
-    const PagedItem it = paged_item(p, i, groups);
+    const PagedItem it = paged_item(p, list.begin + i);
     const PagedSpan<BN, kMaxRows> sp(it, group_heads);
     units += sp.units(p.num_kv_heads);
     rows += sp.part_rows(p.num_kv_heads);
     if (blockIdx.x == 0) {
-      if (i < groups) {
-        bad |= it.t1 > it.t0 && p.prefix_lens[i] != paged_clamp_len(p, p.prefix_lens[i]);
+      const int g = list.begin + i;
+      if (g < p.num_groups) {
+        bad |= it.t1 > it.t0 && p.prefix_lens[g] != paged_clamp_len(p, p.prefix_lens[g]);
       } else {
-        bad |= p.kv_lens[i - groups] != it.hi;
+        bad |= p.kv_lens[g - p.num_groups] != it.hi;
       }
     }
   }
@@ -177,23 +192,23 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
   if (find || blockIdx.x == 0) {
     long long u = base_u, r = base_r;
     for (int i = i0; i < i1; ++i) {
-      const PagedItem it = paged_item(p, i, groups);
+      const PagedItem it = paged_item(p, list.begin + i);
       const PagedSpan<BN, kMaxRows> sp(it, group_heads);
       const long long du = sp.units(p.num_kv_heads);
       if (du > 0 && u <= mine && mine < u + du) {
-        sc->item = i;
+        sc->item = list.begin + i;
         sc->item_unit = u;
         sc->item_row = r;
       }
       if (blockIdx.x == 0) {
-        items[i] = u;
-        items[n + 1 + i] = r;
+        list.items[i] = u;
+        list.items[n + 1 + i] = r;
       }
       u += du;
       r += sp.part_rows(p.num_kv_heads);
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) items[n] = total;
+  if (blockIdx.x == 0 && threadIdx.x == 0) list.items[n] = total;
   __syncthreads();
 }
 
@@ -201,7 +216,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
 template <int BN, int kMaxRows>
 struct PagedWalk {
   const PagedArgs* p;
-  int group_heads, groups;
+  int group_heads, end;
   int i;
   PagedItem it;
   int tm, rt, first, nt;
@@ -209,7 +224,7 @@ struct PagedWalk {
   int seg, kt, count;  // current piece: segment, first key tile (of the item), tiles
 
   __device__ __forceinline__ void load() {
-    it = paged_item(*p, i, groups);
+    it = paged_item(*p, i);
     const PagedSpan<BN, kMaxRows> sp(it, group_heads);
     tm = sp.tm;
     rt = sp.rt;
@@ -217,10 +232,10 @@ struct PagedWalk {
     nt = sp.nt;
   }
   // false: no work for this CTA
-  __device__ __forceinline__ bool init(const PagedArgs* args, int gh, int ngroups, const PagedScan* sc) {
+  __device__ __forceinline__ bool init(const PagedArgs* args, int gh, const PagedList& list, const PagedScan* sc) {
     p = args;
     group_heads = gh;
-    groups = ngroups;
+    end = list.end;
     const long long u0 = paged_first_unit(blockIdx.x, sc->total, gridDim.x);
     left = paged_first_unit(blockIdx.x + 1, sc->total, gridDim.x) - u0;
     if (left <= 0) return false;
@@ -241,7 +256,7 @@ struct PagedWalk {
       seg = 0;
       do {
         item_row += static_cast<long long>(p->num_kv_heads) * rt * tm;
-        if (++i >= groups + p->num_seqs) return false;
+        if (++i >= end) return false;
         load();
       } while (nt == 0);
     }

@@ -26,8 +26,11 @@
 namespace dhsa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Groups of more rows (query tokens times Hq / Hkv) than this have their
+// prefixes worked on by the tcgen05 kernel.
+constexpr int kOwnPrefixRows = 32;
 
 // ------------------------------------------------------------------ bf16
 constexpr int kBN = 64;        // keys a tile
@@ -49,16 +52,6 @@ struct MmaCfg {
   static constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16 + 1024;
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
-
-// 4-D tiled load (no multicast) into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                            int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -144,7 +137,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     qrow[e] = nullptr;
     if (r < rows) {
       const int t = k.it.t0 + r / gh;
-      const int b = k.i < k.groups ? paged_seq_of(w.p, t) : k.it.row;
+      const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
       lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
       qrow[e] = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride + static_cast<long long>(h * gh + r % gh) * D;
     }
@@ -323,7 +316,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
       const float2 v = ml[(g * WN + x) * 16 + r];
       sum += v.y * (top == -INFINITY ? 1.f : ex2_approx(v.x - top));
     }
-    w.part_ml[part + threadIdx.x] = make_float2(top, sum);
+    w.list.part_ml[part + threadIdx.x] = make_float2(top, sum);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -348,7 +341,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
         a.z += u.z;
         a.w += u.w;
       }
-      *reinterpret_cast<float4*>(w.part_o + (part + r) * D + c * (D / 4) + 4 * v) = a;
+      *reinterpret_cast<float4*>(w.list.part_o + (part + r) * D + c * (D / 4) + 4 * v) = a;
     }
     if (c < 3) compute_sync();
   }
@@ -358,7 +351,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
 template <int D>
 __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ PagedWork w, int groups) {
+                     const __grid_constant__ PagedWork w) {
   using C = MmaCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -385,10 +378,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, groups, w.items, sc, w.status);  // syncs the CTA
+  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, w.list, sc, w.status);  // syncs the CTA
 
   PagedWalk<kBN, kMaxRows> walk;
-  if (!walk.init(&w.p, gh, groups, sc)) return;  // uniform for the CTA
+  if (!walk.init(&w.p, gh, w.list, sc)) return;  // uniform for the CTA
 
   if (warp == kProducer) {
     // a lane for each box of a tile: (page part, 64-column slice, K or V)
@@ -476,7 +469,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 
 template <int D>
 __global__ void __launch_bounds__(kFThreads)
-    paged_f32_kernel(const __grid_constant__ PagedWork w, int groups) {
+    paged_f32_kernel(const __grid_constant__ PagedWork w) {
   using C = F32Cfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   float* kv = reinterpret_cast<float*>(smem_raw);
@@ -485,9 +478,9 @@ __global__ void __launch_bounds__(kFThreads)
   PagedScan* sc = reinterpret_cast<PagedScan*>(smem_raw + C::kOffScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gh = w.num_q_heads / w.p.num_kv_heads;
-  paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, groups, w.items, sc, w.status);
+  paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, w.list, sc, w.status);
   PagedWalk<kFBN, kFRows> k;
-  if (!k.init(&w.p, gh, groups, sc)) return;
+  if (!k.init(&w.p, gh, w.list, sc)) return;
   const float scale_log2 = w.scale * kLog2e;
   do {
     const int h = k.seg / k.rt, rt = k.seg - h * k.rt;
@@ -539,7 +532,7 @@ __global__ void __launch_bounds__(kFThreads)
       lim[e] = 0;
       if (r < rows) {
         const int t = k.it.t0 + r / gh;
-        const int b = k.i < groups ? paged_seq_of(w.p, t) : k.it.row;
+        const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
         lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
       }
       m[e] = -INFINITY;
@@ -607,9 +600,9 @@ __global__ void __launch_bounds__(kFThreads)
       for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       const int r = warp * 4 + e;
       if (row0 + r < rows) {
-        if (lane == 0) w.part_ml[part + r] = make_float2(m[e], sum);
+        if (lane == 0) w.list.part_ml[part + r] = make_float2(m[e], sum);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) w.part_o[(part + r) * D + c * 32 + lane] = o[e][c];
+        for (int c = 0; c < kCols; ++c) w.list.part_o[(part + r) * D + c * 32 + lane] = o[e][c];
       }
     }
   } while (k.next());
@@ -619,7 +612,7 @@ __global__ void __launch_bounds__(kFThreads)
 // One CTA for each (token, head): the partials of the row's prefix segment and
 // of its own segment, in the order of the CTAs that made them.
 template <int D, typename T, int BN, int kMax>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w, int groups, int ctas) {
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
   constexpr int kCols = D / 32;
   const int t = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -631,35 +624,45 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     if (w.lse != nullptr && threadIdx.x == 0) w.lse[static_cast<long long>(t) * w.num_q_heads + h] = -INFINITY;
     return;
   }
-  const int n = groups + w.p.num_seqs;
-  const long long total = w.items[n];
-  // the row's two segments: partial rows part[x] + j * kMax for j < count[x]
-  long long part[2];
-  int count[2] = {0, 0};
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    part[x] = 0;
-    if (x == 0 && groups == 0) continue;
-    const int i = x == 0 ? paged_group_of(w.p, b) : groups + b;
-    const PagedItem it = paged_item(w.p, i, groups);
-    const PagedSpan<BN, kMax> sp(it, gh);
-    if (sp.nt == 0) continue;
+  // the row's partials of one item: rows at + j * step for j < count
+  struct Parts {
+    const float* o;
+    const float2* ml;
+    long long at;
+    int step, count;
+  };
+  auto parts_of = [&](auto span, const PagedList& l, int i) -> Parts {
+    using Span = decltype(span);
+    Parts x{l.part_o, l.part_ml, 0, Span::kMax, 0};
+    const PagedItem it = paged_item(w.p, i);
+    const Span sp(it, gh);
+    if (sp.nt == 0) return x;
+    const int n = l.end - l.begin, j = i - l.begin;
+    const long long total = l.items[n];
     const int r = (t - it.t0) * gh + h % gh;
     const int seg = (h / gh) * sp.rt + r / sp.tm;
-    const long long u0 = w.items[i] + static_cast<long long>(seg) * sp.nt;
-    const int c0 = paged_owner(u0, total, ctas), c1 = paged_owner(u0 + sp.nt - 1, total, ctas);
-    part[x] = paged_part_row(c0, kMax, w.items[n + 1 + i], seg, sp.tm) + r % sp.tm;
-    count[x] = c1 - c0 + 1;
-  }
-  const int all = count[0] + count[1];
-  auto row_of = [&](int j) -> long long {
-    return j < count[0] ? part[0] + static_cast<long long>(j) * kMax
-                        : part[1] + static_cast<long long>(j - count[0]) * kMax;
+    const long long u0 = l.items[j] + static_cast<long long>(seg) * sp.nt;
+    const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + sp.nt - 1, total, l.ctas);
+    x.at = paged_part_row(c0, Span::kMax, l.items[n + 1 + j], seg, sp.tm) + r % sp.tm;
+    x.count = c1 - c0 + 1;
+    return x;
   };
+  Parts pre{nullptr, nullptr, 0, 0, 0};
+  if (w.p.num_groups > 0) {
+    const int g = paged_group_of(w.p, b);
+    pre = w.prefix.end > 0 ? parts_of(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g)
+                           : parts_of(PagedSpan<BN, kMax>(), w.list, g);
+  }
+  const Parts own = parts_of(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
+  const int all = pre.count + own.count;
   __shared__ float red[4];
   __shared__ float acc_s[4][D + 1];
   float top = -INFINITY;
-  for (int j = threadIdx.x; j < all; j += 128) top = fmaxf(top, w.part_ml[row_of(j)].x);
+  for (int j = threadIdx.x; j < all; j += 128) {
+    const Parts& x = j < pre.count ? pre : own;
+    const int i = j < pre.count ? j : j - pre.count;
+    top = fmaxf(top, x.ml[x.at + static_cast<long long>(i) * x.step].x);
+  }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) red[warp] = top;
@@ -671,12 +674,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
 #pragma unroll 4
   for (int j = warp; j < all; j += 4) {
-    const long long r = row_of(j);
-    const float2 v = w.part_ml[r];
+    const Parts& x = j < pre.count ? pre : own;
+    const int i = j < pre.count ? j : j - pre.count;
+    const long long r = x.at + static_cast<long long>(i) * x.step;
+    const float2 v = x.ml[r];
     const float f = ex2_approx(v.x - base);
     sum += v.y * f;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(w.part_o[r * D + c * 32 + lane], f, acc[c]);
+    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(x.o[r * D + c * 32 + lane], f, acc[c]);
   }
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
@@ -690,23 +695,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     w.lse[static_cast<long long>(t) * w.num_q_heads + h] = (top + log2f(l)) * kLn2;
 }
 
-// (d, page_size, Hkv, pages) view of a 16-bit page array; one box is 64 columns
-// of up to 64 tokens of a page, rows of 128 bytes, swizzled.
-CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, bool f16) {
-  const TensorMapEncodeFn fn = tensor_map_encode_fn();
-  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.page_size),
-                              static_cast<cuuint64_t>(p.num_kv_heads), static_cast<cuuint64_t>(p.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.head_dim) * 2,
-                                 static_cast<cuuint64_t>(p.page_size) * p.head_dim * 2,
-                                 static_cast<cuuint64_t>(p.page_stride) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page_size < kBN ? p.page_size : kBN), 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
 int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -715,81 +703,109 @@ int sm_count() {
   return sms;
 }
 
-// CTAs of the grid at most: what the partials are sized for.
+// CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
 
 template <int D, typename T, int BN, int kMax>
-cudaError_t join(const PagedWork& w, int groups, int ctas, cudaStream_t stream) {
-  paged_join_kernel<D, T, BN, kMax><<<dim3(w.p.total_q, w.num_q_heads), 128, 0, stream>>>(w, groups, ctas);
+cudaError_t join(const PagedWork& w, cudaStream_t stream) {
+  paged_join_kernel<D, T, BN, kMax><<<dim3(w.p.total_q, w.num_q_heads), 128, 0, stream>>>(w);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run_mma(const PagedWork& w, int groups, cudaStream_t stream) {
+cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   using C = MmaCfg<D>;
   CUtensorMap mk, mv;
-  if (encode_pages_map(&mk, w.p.k_pages, w.p, false) != CUDA_SUCCESS ||
-      encode_pages_map(&mv, w.p.v_pages, w.p, true) != CUDA_SUCCESS)
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, false) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, true) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int ctas = sm_count() * C::kCtas < kMaxCtas ? sm_count() * C::kCtas : kMaxCtas;
-  if (ctas <= 0) return cudaErrorInvalidDevice;
-  paged_mma_kernel<D><<<ctas, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w, groups);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  w.list.ctas = sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas;
+  if (w.prefix.end > 0) {
+    w.prefix.ctas = paged_prefix_ctas(D, sms) < kMaxCtas ? paged_prefix_ctas(D, sms) : kMaxCtas;
+    if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
+  }
+  paged_mma_kernel<D><<<w.list.ctas, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return join<D, __nv_bfloat16, kBN, kMaxRows>(w, groups, ctas, stream);
+  return join<D, __nv_bfloat16, kBN, kMaxRows>(w, stream);
 }
 
 template <int D>
-cudaError_t run_f32(const PagedWork& w, int groups, cudaStream_t stream) {
+cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   using C = F32Cfg<D>;
   cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int per_sm = D == 256 ? 1 : D == 128 ? 2 : 3;
-  const int ctas = sm_count() * per_sm < kMaxCtas ? sm_count() * per_sm : kMaxCtas;
-  if (ctas <= 0) return cudaErrorInvalidDevice;
-  paged_f32_kernel<D><<<ctas, kFThreads, C::kSmemBytes, stream>>>(w, groups);
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  w.list.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+  paged_f32_kernel<D><<<w.list.ctas, kFThreads, C::kSmemBytes, stream>>>(w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return join<D, float, kFBN, kFRows>(w, groups, ctas, stream);
+  return join<D, float, kFBN, kFRows>(w, stream);
 }
 
 }  // namespace
 
+// (d, page_size, Hkv, pages) view of a 16-bit page array; one box is 64 columns
+// of up to `tile` tokens of a page, rows of 128 bytes, swizzled.
+CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16) {
+  const TensorMapEncodeFn fn = tensor_map_encode_fn();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.page_size),
+                              static_cast<cuuint64_t>(p.num_kv_heads), static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.head_dim) * 2,
+                                 static_cast<cuuint64_t>(p.page_size) * p.head_dim * 2,
+                                 static_cast<cuuint64_t>(p.page_stride) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page_size < tile ? p.page_size : tile), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group_ptr, int num_q_heads, int dtype) {
-  PagedShape s;
-  s.num_items = p.num_groups + p.num_seqs;
+  PagedShape s{};
   const int gh = num_q_heads / p.num_kv_heads;
-  const int max_rows = dtype == DHSA_BF16 ? kMaxRows : kFRows;
-  long long rows = 0;
-  auto add = [&](long long r) {
-    const int tm = dtype == DHSA_BF16 ? paged_tile_rows<kMaxRows>(static_cast<int>(r))
-                                      : paged_tile_rows<kFRows>(static_cast<int>(r));
-    rows += (r + tm - 1) / tm * tm;
+  const bool bf16 = dtype == DHSA_BF16;
+  auto padded = [](long long r, int tm) { return (r + tm - 1) / tm * tm; };
+  auto list_rows = [&](long long r) {
+    return padded(r, bf16 ? paged_tile_rows<kMaxRows>(static_cast<int>(r)) : kFRows);
   };
-  for (int g = 0; g < p.num_groups; ++g)
-    add(static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh);
-  for (int b = 0; b < p.num_seqs; ++b) add(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);
-  s.part_rows = rows * p.num_kv_heads + static_cast<long long>(kMaxCtas) * max_rows;
+  long long most = 0, prefix = 0, list = 0, groups_in_list = 0;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const long long r = static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
+    most = r > most ? r : most;
+    prefix += padded(r, paged_tile_rows<kPrefixRows>(static_cast<int>(r)));
+    groups_in_list += list_rows(r);
+  }
+  for (int b = 0; b < p.num_seqs; ++b) list += list_rows(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);
+  s.own_prefix = bf16 && most > kOwnPrefixRows;
+  s.prefix_items = s.own_prefix ? p.num_groups : 0;
+  s.list_items = p.num_groups + p.num_seqs - s.prefix_items;
+  s.prefix_rows = s.own_prefix ? prefix * p.num_kv_heads + static_cast<long long>(kMaxCtas) * kPrefixRows : 0;
+  s.list_rows = (list + (s.own_prefix ? 0 : groups_in_list)) * p.num_kv_heads +
+                static_cast<long long>(kMaxCtas) * (bf16 ? kMaxRows : kFRows);
   return s;
 }
 
-cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream) {
-  (void)shape;
+cudaError_t launch_paged_attention(const PagedWork& w, int dtype, cudaStream_t stream) {
   if (w.p.total_q <= 0) return cudaSuccess;
-  const int groups = w.p.num_groups;
   if (dtype == DHSA_BF16) {
     switch (w.p.head_dim) {
-      case 64: return run_mma<64>(w, groups, stream);
-      case 128: return run_mma<128>(w, groups, stream);
-      default: return run_mma<256>(w, groups, stream);
+      case 64: return run_mma<64>(w, stream);
+      case 128: return run_mma<128>(w, stream);
+      default: return run_mma<256>(w, stream);
     }
   }
   switch (w.p.head_dim) {
-    case 64: return run_f32<64>(w, groups, stream);
-    case 128: return run_f32<128>(w, groups, stream);
-    default: return run_f32<256>(w, groups, stream);
+    case 64: return run_f32<64>(w, stream);
+    case 128: return run_f32<128>(w, stream);
+    default: return run_f32<256>(w, stream);
   }
 }
 

@@ -2,6 +2,7 @@
 // rotary positions, paged append and paged attention (C++ linkage, not exported).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -44,11 +45,20 @@ cudaError_t launch_kv_append(const PagedArgs& a, int dtype, const dhsa_rope_tabl
 
 // Paged attention.  The work of a call is a list of items, each a set of query
 // tokens that walk one range of keys: the groups' shared prefixes first, then
-// every sequence's own part.  An item has Hkv * ceil(rows / kTileRows-sized
-// tiles) segments (rows = its tokens times Hq / Hkv), each of all its key
-// tiles; the key tiles of all segments, in order, are cut evenly among `ctas`
-// CTAs, and a CTA leaves one partial result (O unnormalised, running max, sum)
-// for each segment that it touches.
+// every sequence's own part.  An item has Hkv * ceil(rows / its tile's rows)
+// segments (rows = its tokens times Hq / Hkv), each of all its key tiles; the
+// key tiles of all segments, in order, are cut evenly among the CTAs, and a CTA
+// leaves one partial result (O unnormalised, running max, sum) for each segment
+// that it touches.  One kernel works on one list: all items, or the prefixes
+// and the sequences in a list each.
+struct PagedList {
+  int begin, end;    // items of the list
+  int ctas;          // CTAs of its grid
+  float* part_o;     // [rows of all its partials, d]
+  float2* part_ml;   // [rows of all its partials]: running max (log2 units), sum
+  long long* items;  // [2 (end - begin) + 1]: first key tile of each item, the total, then first row of each item
+};
+
 struct PagedWork {
   PagedArgs p;
   const void* q;
@@ -58,19 +68,29 @@ struct PagedWork {
   float* lse;  // may be null
   int num_q_heads;
   float scale;
-  float* part_o;    // [rows of all partials, d]
-  float2* part_ml;  // [rows of all partials]: running max (log2 units), sum
-  long long* items; // [2 * num_items + 1]: first key tile of each item, the total, then first row of each item
+  PagedList prefix;  // the groups, where they are a list of their own; else empty
+  PagedList list;    // the sequences, and the groups where `prefix` is empty
   uint32_t* status;
 };
 
-// Rows of partials that a call may need at most, from the host mirrors.
+// How a call divides into lists, and the rows of partials that they may need at
+// most (from the host mirrors).
 struct PagedShape {
-  int num_items;
-  long long part_rows;
+  bool own_prefix;  // the prefixes are a list of their own
+  int prefix_items, list_items;
+  long long prefix_rows, list_rows;
 };
 PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group_ptr, int num_q_heads, int dtype);
 
-cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedWork& w, int dtype, cudaStream_t stream);
+
+// TMA view of a 16-bit page array; one box is 64 columns of up to `tile` tokens of a page.
+CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16);
+
+// The prefixes' list on tcgen05 (bf16): tiles of 128 rows and 128 keys.
+constexpr int kPrefixBN = 128;
+constexpr int kPrefixRows = 128;
+int paged_prefix_ctas(int head_dim, int sms);
+cudaError_t launch_paged_prefix(const PagedWork& w, cudaStream_t stream);
 
 }  // namespace dhsa

@@ -231,6 +231,15 @@ ATTEND_CASES = {
     "two_groups": (BF16, 8, 1, 128, 64, [1] * 7, [300, 280, 257, 500, 66, 70, 64], ([0, 4, 7], [256, 33]), "peaks"),
     "empty_group": (BF16, 4, 2, 64, 16, [1] * 3, [40, 50, 60], ([0, 0, 2, 3, 3], [77, 32, 0, 16]), "normal"),
     "prefix_rows": (BF16, 8, 2, 128, 16, [1] * 40, [600 + 7 * i for i in range(40)], ([0, 40], [600]), "peaks"),
+    # many rows on one prefix: d 64 / 128 / 256, rows beyond one tile, a prefix that ends inside a tile, in a page
+    "many_d64": (BF16, 16, 2, 64, 128, [1] * 30, [1300 + 11 * i for i in range(30)], ([0, 30], [1291]), "peaks"),
+    "many_d128": (BF16, 32, 4, 128, 32, [2] * 21, [2600 + 7 * i for i in range(21)], ([0, 21], [2590]), "peaks"),
+    "many_d256": (BF16, 8, 2, 256, 16, [3] * 25, [900 + 3 * i for i in range(25)], ([0, 25], [833]), "peaks"),
+    "many_groups": (BF16, 8, 1, 128, 64, [1] * 41, [700 + i for i in range(41)],
+                    ([0, 6, 6, 36, 41], [500, 9, 640, 1]), "peaks"),
+    "many_short_rows": (BF16, 8, 2, 128, 16, [1] * 20, [300] * 5 + [20] * 5 + [0] * 5 + [129] * 5,
+                        ([0, 20], [150]), "normal"),
+    "many_drafted": (BF16, 12, 4, 128, 16, [6] * 16, [130 + i for i in range(16)], ([0, 16], [128]), "normal"),
     "drafted": (BF16, 32, 8, 128, 16, [5] * 5, [405, 431, 410, 500, 417], ([0, 5], [400]), "peaks"),
     "drafted_in_prefix": (BF16, 8, 2, 128, 16, [7] * 4, [205, 203, 220, 190], ([0, 4], [200]), "normal"),
     "heads_odd": (BF16, 21, 3, 128, 16, [1, 2, 3], [33, 77, 150], None, "normal"),
