@@ -484,15 +484,22 @@ def selftest_timeout(limit_us: int = 20000, device=None) -> int:
 # ------------------------------------------------- around the prefill path
 
 
-class _on_device:
-    """Makes a tensor's device the current one for a call (launches and the
-    current stream go by it); nothing to do where it already is."""
+# The calls below cost a few microseconds on the GPU at a decode step, so their
+# marshalling is kept short: device indexes instead of device objects, the raw
+# current stream instead of a Stream object, plain integers for pointers.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, t: torch.Tensor):
-        self.index = t.device.index
+
+class _on_device:
+    """Makes a device the current one for a block (launches go by it); nothing
+    to do where it already is."""
+
+    def __init__(self, index: int):
+        self.index = index
 
     def __enter__(self):
-        self.before = torch.cuda.current_device()
+        self.before = _current_device()
         if self.before != self.index:
             torch.cuda.set_device(self.index)
 
@@ -501,33 +508,52 @@ class _on_device:
             torch.cuda.set_device(self.before)
 
 
+def _call(fn, name: str, index: int, *args) -> None:
+    """fn(*args) with device `index` current; raises on an error status."""
+    if _current_device() == index:
+        code = fn(*args)
+    else:
+        with _on_device(index):
+            code = fn(*args)
+    if code != 0:
+        raise DhsaError(code, name)
+
+
+def _stream_on(stream, index: int) -> int:
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+_NO_TOKENS = _Tokens(None, 0)  # passed by value, never written
+
+
 def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dtype: torch.dtype, tokens: int,
-            device: torch.device) -> _Tokens:
-    """A packed [T, H, d] operand whose tokens may lie apart (a slice of a fused tensor)."""
+            index: int) -> _Tokens:
+    """A packed [T, H, d] operand whose tokens may lie apart (a slice of a fused
+    tensor), on CUDA device `index`."""
     if t is None:
-        return _Tokens(None, 0)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, the call on %s" % (name, t.device, device))
-    if t.dtype != dtype:
+        return _NO_TOKENS
+    if t.get_device() != index:
+        raise ValueError("%s must be a CUDA tensor on device %d, got %s" % (name, index, t.device))
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    s = t.shape
-    if len(s) != 3 or s[0] < tokens or s[1] != heads or s[2] != head_dim:
-        raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(s)))
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+    if t.dim() != 3:
+        raise ValueError("%s must be [T, H, d], got %s" % (name, tuple(t.shape)))
+    n, h, d = t.shape
+    if n < tokens or h != heads or d != head_dim:
+        raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(t.shape)))
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != head_dim and heads > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
-    return _Tokens(t.data_ptr(), st[0] if s[0] > 1 else heads * head_dim)
+    return _Tokens(t.data_ptr(), st if n > 1 else heads * head_dim)
 
 
-def _int32(t: torch.Tensor, name: str, shape, device: torch.device) -> None:
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
-    if t.dtype != torch.int32:
+def _int32(t: torch.Tensor, name: str, shape, index: int) -> None:
+    if t.get_device() != index or index < 0:
+        raise ValueError("%s must be a CUDA tensor on device %d" % (name, index))
+    if t.dtype is not torch.int32:
         raise TypeError("%s must be int32" % name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor, got %s" % (name, shape, tuple(t.shape)))
 
 
 class Rope:
@@ -543,6 +569,7 @@ class Rope:
                  inv_freq=None, factor: float = 1.0):
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.c = _RopeTable()
+        self.ref = ctypes.byref(self.c)
         if inv_freq is not None:
             f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
             if f.shape != (self.rotary_dim // 2,):
@@ -569,29 +596,27 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
     x = q if q is not None else k
     if x is None:
         raise ValueError("rope needs q or k")
-    T, d, dev = x.shape[0], x.shape[-1], x.device
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    T, hq, d = x.shape
+    dev, dtype = x.get_device(), x.dtype
+    hk = 1
     _int32(positions, "positions", (T,), dev)
-    dt = _dtype_code(x)
-    with _on_device(x):
-        args = []
-        outs = []
-        for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if t is None:
-                if out is not None:
-                    raise ValueError("%s_out without %s" % (name, name))
-                args += [_Tokens(None, 0), 1, _Tokens(None, 0)]
-                outs.append(None)
-                continue
-            H = t.shape[1]
-            if out is None:
-                out = torch.empty(T, H, d, dtype=x.dtype, device=dev)
-            args += [_tokens(t, name, H, d, x.dtype, T, dev), H, _tokens(out, name + "_out", H, d, x.dtype, T, dev)]
-            outs.append(out)
+    if q is not None and q_out is None:
+        q_out = torch.empty(T, hq, d, dtype=dtype, device=x.device)
+    if k is not None:
+        hk = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty(T, hk, d, dtype=dtype, device=x.device)
+    if stream is not None:
         _enter(stream)
-        _check(lib().dhsa_rope(ctypes.byref(rope.c), dt, d, T, _ptr(positions), *args, _stream_ptr(stream)),
-               "dhsa_rope")
+    _call(lib().dhsa_rope, "dhsa_rope", dev, rope.ref, _dtype_code(x), d, T, positions.data_ptr(),
+          _tokens(q, "q", hq, d, dtype, T, dev), hq, _tokens(q_out, "q_out", hq, d, dtype, T, dev),
+          _tokens(k, "k", hk, d, dtype, T, dev), hk, _tokens(k_out, "k_out", hk, d, dtype, T, dev),
+          _stream_on(stream, dev))
+    if stream is not None:
         _leave(stream)
-    return tuple(outs)
+    return q_out, k_out
 
 
 class PagedCache:
@@ -618,7 +643,7 @@ class PagedCache:
             raise ValueError("k_pages and v_pages must have one page stride")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = n, h, p, d
-        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.dtype, self.device, self.index = k_pages.dtype, k_pages.device, k_pages.get_device()
         self.c = _PagedCache(_dtype_code(k_pages), h, d, p, n, k_pages.stride(0) if n > 1 else h * p * d,
                              k_pages.data_ptr(), v_pages.data_ptr())
 
@@ -648,8 +673,8 @@ class PagedBatch:
             raise ValueError("cu_q must have B + 1 entries")
         self.num_seqs = int(self.h_cu.shape[0] - 1)
         self.total_tokens = int(self.h_cu[-1])
-        dev = kv_lens.device
-        _int32(kv_lens, "kv_lens", (self.num_seqs,), dev)
+        dev, self.index = kv_lens.device, kv_lens.get_device()
+        _int32(kv_lens, "kv_lens", (self.num_seqs,), self.index)
         if not block_table.is_cuda or block_table.device != dev or block_table.dtype != torch.int32:
             raise ValueError("block_table must be an int32 tensor on %s" % dev)
         if block_table.dim() != 2 or block_table.shape[0] != self.num_seqs or block_table.shape[1] < 1 or \
@@ -667,7 +692,7 @@ class PagedBatch:
             groups = int(self.h_groups.shape[0] - 1)
             if groups < 1:
                 raise ValueError("group_ptr must have G + 1 entries, G >= 1")
-            _int32(prefix_lens, "prefix_lens", (groups,), dev)
+            _int32(prefix_lens, "prefix_lens", (groups,), self.index)
             self.d_groups = torch.from_numpy(self.h_groups).to(dev)
         self.c = _PagedBatch(self.num_seqs, width, stride, groups, self.d_cu.data_ptr(), kv_lens.data_ptr(),
                              block_table.data_ptr(), 0 if groups == 0 else self.d_groups.data_ptr(),
@@ -685,7 +710,8 @@ class KvAppender:
             raise ValueError("cache and batch are on different devices")
         self.cache, self.batch, self.rope = cache, batch, rope
         self.ws = torch.zeros(256, dtype=torch.uint8, device=cache.device)
-        self._refs = (ctypes.byref(cache.c), ctypes.byref(batch.c), None if rope is None else ctypes.byref(rope.c))
+        self._fixed = (ctypes.byref(cache.c), ctypes.byref(batch.c), None if rope is None else rope.ref)
+        self._fn, self._ws = lib().dhsa_kv_append, self.ws.data_ptr()
 
     def __call__(self, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
@@ -693,24 +719,24 @@ class KvAppender:
         """Stores k and v [T, Hkv, d]; returns (q_out, k_out): q [T, Hq, d]
         rotated (made where q comes without q_out) and, where given, k_out."""
         c, T = self.cache, self.batch.total_tokens
-        hq, d, dt, dev = (1 if q is None else q.shape[1]), c.head_dim, c.dtype, c.device
-        if q is None and q_out is not None:
+        hk, d, dt, dev, hq, pos = c.num_kv_heads, c.head_dim, c.dtype, c.index, 1, None
+        if q is not None:
+            hq = q.shape[1]
+            if q_out is None:
+                q_out = torch.empty(T, hq, d, dtype=dt, device=c.device)
+        elif q_out is not None:
             raise ValueError("q_out without q")
         if positions is not None:
             _int32(positions, "positions", (T,), dev)
-        with _on_device(self.ws):
-            if q is not None and q_out is None:
-                q_out = torch.empty(T, hq, d, dtype=dt, device=dev)
-            _check(lib().dhsa_kv_append(
-                self._refs[0], self._refs[1], self._refs[2], _ptr(positions),
-                _tokens(k, "k", c.num_kv_heads, d, dt, T, dev), _tokens(v, "v", c.num_kv_heads, d, dt, T, dev),
-                _tokens(k_out, "k_out", c.num_kv_heads, d, dt, T, dev), _tokens(q, "q", hq, d, dt, T, dev),
-                _tokens(q_out, "q_out", hq, d, dt, T, dev), hq, _ptr(self.ws), 256, _stream_ptr(stream)),
-                "dhsa_kv_append")
+            pos = positions.data_ptr()
+        _call(self._fn, "dhsa_kv_append", dev, *self._fixed, pos, _tokens(k, "k", hk, d, dt, T, dev),
+              _tokens(v, "v", hk, d, dt, T, dev), _tokens(k_out, "k_out", hk, d, dt, T, dev),
+              _tokens(q, "q", hq, d, dt, T, dev), _tokens(q_out, "q_out", hq, d, dt, T, dev), hq, self._ws, 256,
+              _stream_on(stream, dev))
         return q_out, k_out
 
     def status(self, stream=None) -> int:
-        with _on_device(self.ws):
+        with _on_device(self.cache.index):
             return lib().dhsa_workspace_status(_ptr(self.ws), _stream_ptr(stream))
 
     def reset(self) -> None:
@@ -724,7 +750,7 @@ def append_kv(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: torch.Te
               check: bool = False):
     """One-shot append to the paged cache; returns (q_out, k_out) as KvAppender does."""
     a = KvAppender(cache, batch, rope)
-    with _on_device(a.ws):
+    with _on_device(cache.index):
         _enter(stream)
         if q is not None and q_out is None:
             q_out = torch.empty(batch.total_tokens, q.shape[1], cache.head_dim, dtype=cache.dtype,
@@ -751,24 +777,25 @@ class PagedAttention:
                "dhsa_paged_attention_workspace_size")
         self.ws = _workspace(n.value, cache.device)
         self.reset()
-        self._refs = (ctypes.byref(cache.c), ctypes.byref(batch.c))
+        self._fixed = (ctypes.byref(cache.c), ctypes.byref(batch.c))
+        self._fn, self._ws, self._ws_bytes = lib().dhsa_paged_attention, self.ws.data_ptr(), self.ws.numel()
 
     def __call__(self, q: torch.Tensor, out: torch.Tensor, scale: Optional[float] = None,
                  lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         c, T, hq = self.cache, self.batch.total_tokens, self.num_q_heads
-        dev = c.device
-        if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous()
-                                or lse.dim() != 2 or lse.shape[0] < T or lse.shape[1] != hq):
-            raise ValueError("lse must be a contiguous float32 [>= %d, %d] tensor on %s" % (T, hq, dev))
-        with _on_device(self.ws):
-            _check(lib().dhsa_paged_attention(
-                self._refs[0], self._refs[1], _tokens(q, "q", hq, c.head_dim, c.dtype, T, dev), hq,
-                0.0 if scale is None else scale, _tokens(out, "out", hq, c.head_dim, c.dtype, T, dev), _ptr(lse),
-                _ptr(self.ws), self.ws.numel(), _stream_ptr(stream)), "dhsa_paged_attention")
+        d, dt, dev, lse_ptr = c.head_dim, c.dtype, c.index, None
+        if lse is not None:
+            if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous() \
+                    or lse.dim() != 2 or lse.shape[0] < T or lse.shape[1] != hq:
+                raise ValueError("lse must be a contiguous float32 [>= %d, %d] tensor on device %d" % (T, hq, dev))
+            lse_ptr = lse.data_ptr()
+        _call(self._fn, "dhsa_paged_attention", dev, *self._fixed, _tokens(q, "q", hq, d, dt, T, dev), hq,
+              0.0 if scale is None else scale, _tokens(out, "out", hq, d, dt, T, dev), lse_ptr, self._ws,
+              self._ws_bytes, _stream_on(stream, dev))
         return out
 
     def status(self, stream=None) -> int:
-        with _on_device(self.ws):
+        with _on_device(self.cache.index):
             return lib().dhsa_workspace_status(_ptr(self.ws), _stream_ptr(stream))
 
     def reset(self) -> None:
@@ -781,7 +808,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatch, scale
     """Attention of the new tokens q [T, Hq, d] over the paged cache.  Rows of
     the result behind the last sequence's are zero."""
     a = PagedAttention(cache, batch, q.shape[1])
-    with _on_device(a.ws):
+    with _on_device(cache.index):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         out[batch.total_tokens:].zero_()
         _enter(stream)
