@@ -19,6 +19,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Programmatic dependent launch: a call's later kernels are launched while the
+// earlier ones run.  `let_next_start` is given by every CTA of a kernel (or by
+// its exit); `wait_for_previous` returns when the kernel before has completed
+// and its writes are visible.  The prefixes' kernel and the list's kernel read
+// the call's inputs only, so the second need not wait for the first to begin,
+// but it waits before it ends: its completion then stands for both.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One item: the query tokens [t0, t1) over the keys [lo, hi) of a table row.
 struct PagedItem {
   int t0, t1, lo, hi, row;
@@ -114,12 +123,17 @@ struct PagedSpan {
 __device__ __forceinline__ int paged_ctas(long long total, int ctas) {
   return static_cast<int>(min(total, static_cast<long long>(ctas)));
 }
+// (Products within 32 bits, the usual case, divide several times faster.)
+__device__ __forceinline__ long long paged_divide(long long a, long long b) {
+  if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 __device__ __forceinline__ long long paged_first_unit(long long c, long long total, int ctas) {
   const int n = paged_ctas(total, ctas);
-  return c < n ? c * total / n : total;
+  return c < n ? paged_divide(c * total, n) : total;
 }
 __device__ __forceinline__ int paged_owner(long long unit, long long total, int ctas) {
-  return static_cast<int>(((unit + 1) * paged_ctas(total, ctas) - 1) / total);
+  return static_cast<int>(paged_divide((unit + 1) * paged_ctas(total, ctas) - 1, total));
 }
 
 // Where CTA c's partial of a segment starts (rows): c steps by the largest
@@ -243,7 +257,7 @@ struct PagedWalk {
     item_row = sc->item_row;
     load();
     const long long off = u0 - sc->item_unit;
-    seg = static_cast<int>(off / nt);
+    seg = static_cast<int>(paged_divide(off, nt));
     kt = static_cast<int>(off - static_cast<long long>(seg) * nt);
     count = static_cast<int>(min(static_cast<long long>(nt - kt), left));
     return true;

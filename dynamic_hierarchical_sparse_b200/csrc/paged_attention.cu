@@ -380,8 +380,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
   }
   paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, w.list, sc, w.status);  // syncs the CTA
 
+  let_next_start();
   PagedWalk<kBN, kMaxRows> walk;
-  if (!walk.init(&w.p, gh, w.list, sc)) return;  // uniform for the CTA
+  if (!walk.init(&w.p, gh, w.list, sc)) {  // uniform for the CTA
+    wait_for_previous();
+    return;
+  }
 
   if (warp == kProducer) {
     // a lane for each box of a tile: (page part, 64-column slice, K or V)
@@ -445,6 +449,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
       }
     } while (ok && walk.next());
   }
+  wait_for_previous();  // of the prefixes' kernel, see paged.cuh
 }
 
 // ------------------------------------------------------------------ fp32
@@ -479,6 +484,7 @@ __global__ void __launch_bounds__(kFThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gh = w.num_q_heads / w.p.num_kv_heads;
   paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, w.list, sc, w.status);
+  let_next_start();
   PagedWalk<kFBN, kFRows> k;
   if (!k.init(&w.p, gh, w.list, sc)) return;
   const float scale_log2 = w.scale * kLog2e;
@@ -610,7 +616,8 @@ __global__ void __launch_bounds__(kFThreads)
 
 // ------------------------------------------------------------------ join
 // One CTA for each (token, head): the partials of the row's prefix segment and
-// of its own segment, in the order of the CTAs that made them.
+// of its own segment, in the order of the CTAs that made them, dealt to four
+// warps, whose results join in the order of the warps.
 template <int D, typename T, int BN, int kMax>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
   constexpr int kCols = D / 32;
@@ -619,78 +626,109 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int gh = w.num_q_heads / w.p.num_kv_heads;
   const int b = paged_seq_of(w.p, t);
   T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
-  if (paged_limit(w.p, b, t) <= 0) {
+  // a row's partials of one item: rows at + j * kStep for j < count
+  struct Place {
+    int seg, nt, tm, in_tile, j, n;  // segment, its key tiles, tile rows, row in the tile; item of its list, items
+  };
+  auto place = [&](auto span, const PagedList& l, int i) -> Place {
+    using Span = decltype(span);
+    const PagedItem it = paged_item(w.p, i);
+    const Span sp(it, gh);
+    const int r = (t - it.t0) * gh + h % gh;
+    return Place{(h / gh) * sp.rt + r / sp.tm, sp.nt, sp.tm, r % sp.tm, i - l.begin, l.end - l.begin};
+  };
+  const bool own_list = w.prefix.end > 0;
+  const int limit = paged_limit(w.p, b, t);
+  Place pp{0, 0, 1, 0, 0, 0};
+  if (w.p.num_groups > 0) {
+    const int g = paged_group_of(w.p, b);
+    pp = own_list ? place(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
+  }
+  const Place po = place(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
+  wait_for_previous();
+  if (limit <= 0) {
     for (int c = threadIdx.x; c < D; c += 128) out[c] = static_cast<T>(0.f);
     if (w.lse != nullptr && threadIdx.x == 0) w.lse[static_cast<long long>(t) * w.num_q_heads + h] = -INFINITY;
     return;
   }
-  // the row's partials of one item: rows at + j * step for j < count
-  struct Parts {
-    const float* o;
-    const float2* ml;
-    long long at;
-    int step, count;
+  auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> long long {
+    count = 0;
+    if (p.nt == 0) return 0;
+    const long long total = l.items[p.n], u0 = l.items[p.j] + static_cast<long long>(p.seg) * p.nt;
+    const long long row = l.items[p.n + 1 + p.j];
+    const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + p.nt - 1, total, l.ctas);
+    count = c1 - c0 + 1;
+    return paged_part_row(c0, step, row, p.seg, p.tm) + p.in_tile;
   };
-  auto parts_of = [&](auto span, const PagedList& l, int i) -> Parts {
-    using Span = decltype(span);
-    Parts x{l.part_o, l.part_ml, 0, Span::kMax, 0};
-    const PagedItem it = paged_item(w.p, i);
-    const Span sp(it, gh);
-    if (sp.nt == 0) return x;
-    const int n = l.end - l.begin, j = i - l.begin;
-    const long long total = l.items[n];
-    const int r = (t - it.t0) * gh + h % gh;
-    const int seg = (h / gh) * sp.rt + r / sp.tm;
-    const long long u0 = l.items[j] + static_cast<long long>(seg) * sp.nt;
-    const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + sp.nt - 1, total, l.ctas);
-    x.at = paged_part_row(c0, Span::kMax, l.items[n + 1 + j], seg, sp.tm) + r % sp.tm;
-    x.count = c1 - c0 + 1;
-    return x;
-  };
-  Parts pre{nullptr, nullptr, 0, 0, 0};
-  if (w.p.num_groups > 0) {
-    const int g = paged_group_of(w.p, b);
-    pre = w.prefix.end > 0 ? parts_of(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g)
-                           : parts_of(PagedSpan<BN, kMax>(), w.list, g);
-  }
-  const Parts own = parts_of(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
-  const int all = pre.count + own.count;
-  __shared__ float red[4];
-  __shared__ float acc_s[4][D + 1];
-  float top = -INFINITY;
-  for (int j = threadIdx.x; j < all; j += 128) {
-    const Parts& x = j < pre.count ? pre : own;
-    const int i = j < pre.count ? j : j - pre.count;
-    top = fmaxf(top, x.ml[x.at + static_cast<long long>(i) * x.step].x);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const float base = top == -INFINITY ? 0.f : top;
-  float acc[kCols], sum = 0.f;
+  const PagedList& pl = own_list ? w.prefix : w.list;
+  const int pstep = own_list ? kPrefixRows : kMax;
+  int pcount, ocount;
+  const long long pfirst = first_row(pp, pl, pstep, pcount);
+  const long long ofirst = first_row(po, w.list, kMax, ocount);
+  const int all = pcount + ocount;
+  float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-#pragma unroll 4
-  for (int j = warp; j < all; j += 4) {
-    const Parts& x = j < pre.count ? pre : own;
-    const int i = j < pre.count ? j : j - pre.count;
-    const long long r = x.at + static_cast<long long>(i) * x.step;
-    const float2 v = x.ml[r];
-    const float f = ex2_approx(v.x - base);
-    sum += v.y * f;
+  constexpr int kBatch = 4;  // partials in flight a warp
+  for (int j0 = warp; j0 < all; j0 += 4 * kBatch) {
+    float2 ml[kBatch];
+    float x[kBatch][kCols];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(x.o[r * D + c * 32 + lane], f, acc[c]);
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + 4 * i;
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
+      if (j < all) {
+        const bool pre = j < pcount;
+        const long long r = pre ? pfirst + static_cast<long long>(j) * pstep
+                                : ofirst + static_cast<long long>(j - pcount) * kMax;
+        ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
+        const float* o = (pre ? pl.part_o : w.list.part_o) + r * D;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) x[i][c] = o[c * 32 + lane];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float f = ex2_approx(m - base);
+    m = top;
+    sum *= f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] *= f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float g = ex2_approx(ml[i].x - base);
+      sum = fmaf(ml[i].y, g, sum);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = fmaf(x[i][c], g, acc[c]);
+    }
   }
+  __shared__ float acc_s[4][D];
+  __shared__ float2 ml_s[4];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
-  if (lane == 0) acc_s[warp][D] = sum;
+  if (lane == 0) ml_s[warp] = make_float2(m, sum);
   __syncthreads();
-  const float l = (acc_s[0][D] + acc_s[1][D]) + (acc_s[2][D] + acc_s[3][D]);
+  float top = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) top = fmaxf(top, ml_s[x].x);
+  const float base = top == -INFINITY ? 0.f : top;
+  float f[4], l = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    f[x] = ex2_approx(ml_s[x].x - base);
+    l = fmaf(ml_s[x].y, f[x], l);
+  }
   const float inv = 1.f / l;
-  for (int c = threadIdx.x; c < D; c += 128)
-    out[c] = static_cast<T>(((acc_s[0][c] + acc_s[1][c]) + (acc_s[2][c] + acc_s[3][c])) * inv);
+  for (int c = threadIdx.x; c < D; c += 128) {
+    float a = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) a = fmaf(acc_s[x][c], f[x], a);
+    out[c] = static_cast<T>(a * inv);
+  }
   if (w.lse != nullptr && threadIdx.x == 0)
     w.lse[static_cast<long long>(t) * w.num_q_heads + h] = (top + log2f(l)) * kLn2;
 }
@@ -703,13 +741,29 @@ int sm_count() {
   return sms;
 }
 
+// `early`: launched while the kernel before it in the stream still runs.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, bool early,
+                         const A&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
 
 template <int D, typename T, int BN, int kMax>
 cudaError_t join(const PagedWork& w, cudaStream_t stream) {
-  paged_join_kernel<D, T, BN, kMax><<<dim3(w.p.total_q, w.num_q_heads), 128, 0, stream>>>(w);
-  return cudaGetLastError();
+  return launch_after(paged_join_kernel<D, T, BN, kMax>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, true, w);
 }
 
 template <int D>
@@ -728,8 +782,7 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
     w.prefix.ctas = paged_prefix_ctas(D, sms) < kMaxCtas ? paged_prefix_ctas(D, sms) : kMaxCtas;
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
   }
-  paged_mma_kernel<D><<<w.list.ctas, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w);
-  e = cudaGetLastError();
+  e = launch_after(paged_mma_kernel<D>, w.list.ctas, kMmaThreads, C::kSmemBytes, stream, w.prefix.end > 0, mk, mv, w);
   if (e != cudaSuccess) return e;
   return join<D, __nv_bfloat16, kBN, kMaxRows>(w, stream);
 }

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
     fence_mbar_init();
   }
   paged_schedule<kBN, kBM, kThreads>(w.p, gh, w.prefix, sc, w.status);  // syncs the CTA
+  let_next_start();
   PagedWalk<kBN, kBM> walk;
   if (!walk.init(&w.p, gh, w.prefix, sc)) return;  // uniform for the CTA
   if (warp == kMma) {
