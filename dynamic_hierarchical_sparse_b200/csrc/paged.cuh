@@ -17,6 +17,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;  // 0: the destination is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Programmatic dependent launch: a call's later kernels are launched while the
@@ -96,16 +101,24 @@ __host__ __device__ __forceinline__ int paged_tile_rows(int rows) {
   return m;
 }
 
-// An item's segments and key tiles.
+template <int kMaxRows>
+__host__ __device__ __forceinline__ int paged_part_tile(int tm) {
+  return kMaxRows == 256 && tm <= 128 ? 2 * tm : tm;
+}
+
+// An item's segments and key tiles.  Lists whose row tiles reach 256 (the
+// prefixes' own, for d 64 and 128) leave two partials of tiles of up to 128 rows.
 template <int BN, int kMaxRows>
 struct PagedSpan {
   static constexpr int kMax = kMaxRows;
   int rows, tm, rt, first, nt;  // rows; rows a tile, row tiles; first key tile, key tiles
+  int pm;                       // rows of a segment's partials
   PagedSpan() = default;
   __device__ __forceinline__ PagedSpan(const PagedItem& it, int group_heads) {
     rows = (it.t1 - it.t0) * group_heads;
     tm = paged_tile_rows<kMaxRows>(rows);
     rt = (rows + tm - 1) / tm;
+    pm = paged_part_tile<kMaxRows>(tm);
     first = it.lo / BN;
     nt = it.hi > it.lo && rows > 0 ? (it.hi + BN - 1) / BN - first : 0;
   }
@@ -113,7 +126,7 @@ struct PagedSpan {
     return static_cast<long long>(num_kv_heads) * rt * nt;
   }
   __device__ __forceinline__ long long part_rows(int num_kv_heads) const {
-    return static_cast<long long>(num_kv_heads) * rt * tm;
+    return static_cast<long long>(num_kv_heads) * rt * pm;
   }
 };
 
@@ -137,10 +150,10 @@ __device__ __forceinline__ int paged_owner(long long unit, long long total, int 
 }
 
 // Where CTA c's partial of a segment starts (rows): c steps by the largest
-// tile, a segment by its own, and along the list either c or the segment moves
+// tile, a segment by its own rows, and along the list either c or the segment moves
 // on, so no two partials overlap.
-__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int tm) {
-  return static_cast<long long>(c) * max_rows + item_row + static_cast<long long>(seg) * tm;
+__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int pm) {
+  return static_cast<long long>(c) * max_rows + item_row + static_cast<long long>(seg) * pm;
 }
 
 // Shared-memory words of the block-wide scan.
@@ -152,13 +165,15 @@ struct PagedScan {
 
 // Every CTA counts the units of all items (each thread a run of them) and finds
 // the item that holds its first unit.  CTA 0 writes the items' first units and
-// rows for the merge.  kThreads threads, all of them call this.
+// rows for the join.  Called by the CTA's last kThreads threads, which meet at
+// barrier 1; the result is for the whole CTA after its next __syncthreads.
 template <int BN, int kMaxRows, int kThreads>
 __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_heads, const PagedList& list,
                                                PagedScan* sc, uint32_t* status) {
   const int n = list.end - list.begin;
   const int per = (n + kThreads - 1) / kThreads;
-  const int i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
+  const int thread = threadIdx.x - (blockDim.x - kThreads);
+  const int i0 = min(thread * per, n), i1 = min(i0 + per, n);
   long long units = 0, rows = 0;
   bool bad = false;
   for (int i = i0; i < i1; ++i) {
@@ -176,7 +191,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     }
   }
   if (bad) report(status, kDevCheck);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = thread & 31, warp = thread >> 5;
   long long iu = units, ir = rows;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -190,7 +205,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     sc->warp_units[warp] = iu;
     sc->warp_rows[warp] = ir;
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
   long long base_u = iu - units, base_r = ir - rows, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     const long long u = sc->warp_units[w];
@@ -201,7 +216,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     total += u;
   }
   const long long mine = paged_first_unit(blockIdx.x, total, gridDim.x);
-  if (threadIdx.x == 0) sc->total = total;
+  if (thread == 0) sc->total = total;
   const bool find = units > 0 && base_u <= mine && mine < base_u + units;
   if (find || blockIdx.x == 0) {
     long long u = base_u, r = base_r;
@@ -222,8 +237,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
       r += sp.part_rows(p.num_kv_heads);
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) list.items[n] = total;
-  __syncthreads();
+  if (blockIdx.x == 0 && thread == 0) list.items[n] = total;
 }
 
 // A CTA's walk over its pieces: consecutive key tiles of one segment each.
@@ -233,7 +247,7 @@ struct PagedWalk {
   int group_heads, end;
   int i;
   PagedItem it;
-  int tm, rt, first, nt;
+  int tm, pm, rt, first, nt;
   long long item_row, left;
   int seg, kt, count;  // current piece: segment, first key tile (of the item), tiles
 
@@ -241,6 +255,7 @@ struct PagedWalk {
     it = paged_item(*p, i);
     const PagedSpan<BN, kMaxRows> sp(it, group_heads);
     tm = sp.tm;
+    pm = sp.pm;
     rt = sp.rt;
     first = sp.first;
     nt = sp.nt;
@@ -269,7 +284,7 @@ struct PagedWalk {
     if (++seg == p->num_kv_heads * rt) {
       seg = 0;
       do {
-        item_row += static_cast<long long>(p->num_kv_heads) * rt * tm;
+        item_row += static_cast<long long>(p->num_kv_heads) * rt * pm;
         if (++i >= end) return false;
         load();
       } while (nt == 0);

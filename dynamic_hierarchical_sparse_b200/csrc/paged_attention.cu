@@ -304,7 +304,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
     f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
   }
-  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg, k.tm);
+  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg, k.pm);
   const int valid = min(rows - row0, WM * 16);
   if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
     const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, w.list, sc, w.status);  // syncs the CTA
+  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, w.list, sc, w.status);
+  __syncthreads();
 
   let_next_start();
   PagedWalk<kBN, kMaxRows> walk;
@@ -467,11 +468,6 @@ struct F32Cfg {
   static constexpr int kSmemBytes = kOffScan + static_cast<int>(sizeof(PagedScan));
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  const int n = take ? 16 : 0;  // 0: the destination is zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kFThreads)
     paged_f32_kernel(const __grid_constant__ PagedWork w) {
@@ -484,6 +480,7 @@ __global__ void __launch_bounds__(kFThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gh = w.num_q_heads / w.p.num_kv_heads;
   paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, w.list, sc, w.status);
+  __syncthreads();
   let_next_start();
   PagedWalk<kFBN, kFRows> k;
   if (!k.init(&w.p, gh, w.list, sc)) return;
@@ -598,7 +595,7 @@ __global__ void __launch_bounds__(kFThreads)
       }
       __syncthreads();  // the buffer is free for the tile after next
     }
-    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg, k.tm);
+    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg, k.pm);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float sum = l[e];
@@ -628,18 +625,19 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
   // a row's partials of one item: rows at + j * kStep for j < count
   struct Place {
-    int seg, nt, tm, in_tile, j, n;  // segment, its key tiles, tile rows, row in the tile; item of its list, items
+    int seg, nt, tm, pm, in_tile, j, n;  // segment, its key tiles, tile and partial rows, row in the tile; item, items
   };
   auto place = [&](auto span, const PagedList& l, int i) -> Place {
     using Span = decltype(span);
     const PagedItem it = paged_item(w.p, i);
     const Span sp(it, gh);
     const int r = (t - it.t0) * gh + h % gh;
-    return Place{(h / gh) * sp.rt + r / sp.tm, sp.nt, sp.tm, r % sp.tm, i - l.begin, l.end - l.begin};
+    return Place{(h / gh) * sp.rt + r / sp.tm, sp.nt, sp.tm, sp.pm, r % sp.tm, i - l.begin, l.end - l.begin};
   };
   const bool own_list = w.prefix.end > 0;
   const int limit = paged_limit(w.p, b, t);
-  Place pp{0, 0, 1, 0, 0, 0};
+  constexpr int kPrefixRows = paged_prefix_rows(D);
+  Place pp{0, 0, 1, 1, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
     pp = own_list ? place(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
@@ -658,13 +656,16 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const long long row = l.items[p.n + 1 + p.j];
     const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + p.nt - 1, total, l.ctas);
     count = c1 - c0 + 1;
-    return paged_part_row(c0, step, row, p.seg, p.tm) + p.in_tile;
+    return paged_part_row(c0, step, row, p.seg, p.pm) + p.in_tile;
   };
   const PagedList& pl = own_list ? w.prefix : w.list;
   const int pstep = own_list ? kPrefixRows : kMax;
   int pcount, ocount;
   const long long pfirst = first_row(pp, pl, pstep, pcount);
   const long long ofirst = first_row(po, w.list, kMax, ocount);
+  // a prefix's partials: one a CTA, or two (rows tm apart) where its lanes took turns
+  const int halves = pp.pm > pp.tm ? 1 : 0;
+  pcount <<= halves;
   const int all = pcount + ocount;
   float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
       if (j < all) {
         const bool pre = j < pcount;
-        const long long r = pre ? pfirst + static_cast<long long>(j) * pstep
+        const long long r = pre ? pfirst + static_cast<long long>(j >> halves) * pstep + (halves & j) * pp.tm
                                 : ofirst + static_cast<long long>(j - pcount) * kMax;
         ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
         const float* o = (pre ? pl.part_o : w.list.part_o) + r * D;
@@ -691,7 +692,13 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     }
     float top = m;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+    for (int i = 0; i < kBatch; ++i) {
+      top = fmaxf(top, ml[i].x);
+      if (ml[i].y == 0.f) {  // no weight: O may be unwritten, or 0 * NaN
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
+      }
+    }
     const float base = top == -INFINITY ? 0.f : top;
     const float f = ex2_approx(m - base);
     m = top;
@@ -779,7 +786,7 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.ctas = sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas;
   if (w.prefix.end > 0) {
-    w.prefix.ctas = paged_prefix_ctas(D, sms) < kMaxCtas ? paged_prefix_ctas(D, sms) : kMaxCtas;
+    w.prefix.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
   }
   e = launch_after(paged_mma_kernel<D>, w.list.ctas, kMmaThreads, C::kSmemBytes, stream, w.prefix.end > 0, mk, mv, w);
@@ -829,18 +836,20 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
   auto list_rows = [&](long long r) {
     return padded(r, bf16 ? paged_tile_rows<kMaxRows>(static_cast<int>(r)) : kFRows);
   };
+  const bool wide = paged_prefix_rows(p.head_dim) == 256;
   long long most = 0, prefix = 0, list = 0, groups_in_list = 0;
   for (int g = 0; g < p.num_groups; ++g) {
     const long long r = static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
     most = r > most ? r : most;
-    prefix += padded(r, paged_tile_rows<kPrefixRows>(static_cast<int>(r)));
+    const int tm = wide ? paged_tile_rows<256>(static_cast<int>(r)) : paged_tile_rows<128>(static_cast<int>(r));
+    prefix += (r + tm - 1) / tm * (wide ? paged_part_tile<256>(tm) : tm);
     groups_in_list += list_rows(r);
   }
   for (int b = 0; b < p.num_seqs; ++b) list += list_rows(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);
   s.own_prefix = bf16 && most > kOwnPrefixRows;
   s.prefix_items = s.own_prefix ? p.num_groups : 0;
   s.list_items = p.num_groups + p.num_seqs - s.prefix_items;
-  s.prefix_rows = s.own_prefix ? prefix * p.num_kv_heads + static_cast<long long>(kMaxCtas) * kPrefixRows : 0;
+  s.prefix_rows = s.own_prefix ? prefix * p.num_kv_heads + static_cast<long long>(kMaxCtas) * paged_prefix_rows(p.head_dim) : 0;
   s.list_rows = (list + (s.own_prefix ? 0 : groups_in_list)) * p.num_kv_heads +
                 static_cast<long long>(kMaxCtas) * (bf16 ? kMaxRows : kFRows);
   return s;

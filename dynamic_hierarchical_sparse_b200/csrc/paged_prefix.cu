@@ -3,33 +3,37 @@
 // prefix's keys, each key tile brought from its pages once for the tile of rows.
 //
 // A CTA works on pieces of the prefixes' list (see PagedWork): consecutive
-// 128-key tiles of one (group, KV head, 128-row tile), and leaves each piece's
-// (O unnormalised, running max, sum) for the join.  Per key tile
+// 128-key tiles of one (group, KV head, row tile), and leaves each piece's
+// (O unnormalised, running max, sum) for the join.  Per 128 rows and key tile
 //   S = Q K^T       tcgen05.mma, 128 x 128, into TMEM;
 //   P = exp2(S - m) by four softmax warps, a thread a row, written as f16 over
 //                   S's own columns;
 //   O += P V        tcgen05.mma with A from TMEM, V as stored (f16).
-// One CTA's chain S, softmax, P V has nothing of its own to overlap, so two
-// CTAs share an SM (half of TMEM and of shared memory each for d 64 and 128)
-// and the tensor core works for one while the other's softmax runs; K of the
-// next tile loads during the softmax and V during the next S.  P is handed over
-// in two halves of 64 keys, so the first half's products run beside the second
-// half's exponentials.  d 256 fills TMEM and shared memory alone.
+// That chain has nothing of its own to overlap, so a CTA runs two of them, its
+// lanes, each with its own softmax warpgroup, S, O and issuing thread: the
+// tensor core works for one while the other's softmax runs.  A row tile of more
+// than 128 rows gives each lane half of them and every key tile feeds both; with
+// 128 rows or fewer, where the call is bound by reading keys, both lanes have
+// the same rows and take every other key tile (two partials a piece).  K and V
+// tiles come into rings of 2 and 3 (4 and 4 for d 64).  P is handed over in two
+// halves of 64 keys, so the first half's products run beside the second half's
+// exponentials.  d 256 has TMEM and shared memory for one lane.
 //
-// Warp roles (256 threads): warps 0-3 softmax and the partials' epilogue, warp
-// 4 the TMA producer (a lane for each page part and 64-column slice), warp 5
-// the issue of every MMA; 6 and 7 only give their registers away.
+// The two issuing threads take turns, a tile's P V and the next S to a turn:
+// MMAs of both lanes mixed, one by one, took twice as long (6700 cycles for a
+// key tile of 256 rows).
+//
+// Warp roles: a warpgroup for each lane's softmax, epilogue and Q (cp.async);
+// then a warpgroup of the producer of K tiles (TMA, a lane for each page part
+// and 64-column slice), a warp for each lane's MMAs, and the producer of V tiles.
 #include "launchers.h"
 #include "paged.cuh"
 
 namespace dhsa {
 namespace {
 
-constexpr int kBM = kPrefixRows;
+constexpr int kBM = 128;  // rows of a lane's tile
 constexpr int kBN = kPrefixBN;
-constexpr int kThreads = 256;
-constexpr int kProducer = 4;
-constexpr int kMma = 5;
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last
 // time: weights then reach 256 instead of 1, which f16 holds with the same
 // relative rounding (2^-11), and most tiles skip the pass over O.
@@ -47,38 +51,47 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 template <int D>
 struct PrefixCfg {
-  static constexpr int kCtas = D == 256 ? 1 : 2;  // on an SM
-  static constexpr int kStages = D == 64 ? 2 : 1;  // of the K ring and of the V ring
+  static constexpr int kLanes = D == 256 ? 1 : 2;
+  static constexpr int kRows = paged_prefix_rows(D);  // of a row tile
+  static constexpr int kThreads = 128 * (kLanes + 1);
+  static constexpr int kProducer = 4 * kLanes;
+  static constexpr int kMma = kProducer + 1;  // + lane
+  static constexpr int kProducerV = kProducer + 3;
+  static constexpr int kKStages = D == 256 ? 1 : D == 128 ? 2 : 4;
+  static constexpr int kVStages = D == 256 ? 1 : D == 128 ? 3 : 4;
   static constexpr int kSlices = D / 64;
-  static constexpr int kSub = kBN * 128;           // one 64-column slice of a tile
+  static constexpr int kSub = kBN * 128;  // one 64-column slice of a tile
   static constexpr int kTile = kSlices * kSub;
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTile;
-  static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffScan = kOffV + kStages * kTile;
+  static constexpr int kOffQ = 0;  // + lane
+  static constexpr int kOffK = kLanes * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kTile;
+  static constexpr int kOffScan = kOffV + kVStages * kTile;
   static constexpr int kOffBar = kOffScan + ((static_cast<int>(sizeof(PagedScan)) + 15) / 16) * 16;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
-  static constexpr uint32_t kTmemCols = D == 256 ? 512 : 256;
-  static constexpr uint32_t kColO = D == 256 ? 256 : 128;
-  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0;              // + 128 * lane
+  static constexpr uint32_t kColO = 128 * kLanes;   // + D * lane
+  static_assert(kLanes * (128 + D) <= 512, "TMEM budget");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
 enum {
-  kBarKFull = 0,   // + stage
-  kBarVFull = 2,   // + stage
-  kBarKFree = 4,   // + stage: S of the tile done
-  kBarVFree = 6,   // + stage: P V of the tile done
-  kBarSFull = 8,
-  kBarPHalf = 9,   // first 64 keys of P written, O rescaled
-  kBarPFull = 10,
-  kBarQFull = 11,  // a piece's Q in shared memory
-  kBarODone = 12,  // a piece's last P V done
-  kBarDrain = 13,
-  kNumBars = 14
+  kBarKFull = 0,    // + stage
+  kBarVFull = 4,    // + stage
+  kBarKFree = 8,    // + stage: S of the tile done (one commit a lane, or two of one lane)
+  kBarVFree = 12,   // + stage: P V of the tile done
+  kBarSFull = 16,   // + lane
+  kBarPHalf = 18,   // + lane: first 64 keys of P written, O rescaled
+  kBarPFull = 20,   // + lane
+  kBarQFull = 22,   // + lane: a piece's Q in shared memory
+  kBarODone = 24,   // + lane: a piece's last P V done
+  kBarDrain = 26,   // + lane
+  kBarTurn = 28,    // + lane: that lane's thread ended a turn
+  kNumBars = 30
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
+__global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     paged_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedWork w) {
   using C = PrefixCfg<D>;
@@ -95,21 +108,25 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
   const int gh = w.num_q_heads / w.p.num_kv_heads;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kBarSFull; ++s) mbar_init(bar(s), 1);
-    mbar_init(bar(kBarSFull), 1);
-    mbar_init(bar(kBarPHalf), 4);  // one arrival per softmax warp
-    mbar_init(bar(kBarPFull), 4);
-    mbar_init(bar(kBarQFull), 4);
-    mbar_init(bar(kBarODone), 1);
-    mbar_init(bar(kBarDrain), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(kBarKFull + s), 1);
+      mbar_init(bar(kBarVFull + s), 1);
+      mbar_init(bar(kBarKFree + s), C::kLanes);
+      mbar_init(bar(kBarVFree + s), C::kLanes);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(kBarSFull + a), 1);
+      mbar_init(bar(kBarPHalf + a), 4);  // one arrival per softmax warp
+      mbar_init(bar(kBarPFull + a), 4);
+      mbar_init(bar(kBarQFull + a), 4);
+      mbar_init(bar(kBarODone + a), 1);
+      mbar_init(bar(kBarDrain + a), 1);
+      mbar_init(bar(kBarTurn + a), 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  paged_schedule<kBN, kBM, kThreads>(w.p, gh, w.prefix, sc, w.status);  // syncs the CTA
-  let_next_start();
-  PagedWalk<kBN, kBM> walk;
-  if (!walk.init(&w.p, gh, w.prefix, sc)) return;  // uniform for the CTA
-  if (warp == kMma) {
+  if (warp == C::kMma) {
     tmem_alloc(smem_u32(misc), C::kTmemCols);
     tmem_relinquish();
   }
@@ -117,19 +134,32 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  PagedWalk<kBN, C::kRows> walk{};
+  // Two lanes on one set of rows take every other key tile of a piece
+  // (`apart`): lane a's tiles are a, a + 2, ...; otherwise every one.
+  auto apart = [&]() -> bool { return C::kLanes == 2 && walk.tm <= kBM; };
 
-  if (warp >= 4) {
-    if constexpr (D != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == kProducer) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
+  if (warp >= C::kProducer) {
+    // 8 warps x 224 + 4 x 56 registers = the launch's 12 x 168
+    if constexpr (C::kLanes == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // this warpgroup lays out the CTA's work while the softmax warps warm up
+    paged_schedule<kBN, C::kRows, 128>(w.p, gh, w.prefix, sc, w.status);
+    let_next_start();
+    __syncthreads();
+    const bool work = walk.init(&w.p, gh, w.prefix, sc);
+    if (work && (warp == C::kProducer || warp == C::kProducerV)) {
+      // ------------------------------------------------- K and V producers
       // a lane for each box of a tile: (page part, 64-column slice)
+      const bool is_k = warp == C::kProducer;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      const int full = is_k ? kBarKFull : kBarVFull, free = is_k ? kBarKFree : kBarVFree;
+      const int stages = is_k ? C::kKStages : C::kVStages;
       const int ps = w.p.page_size;
       const int box = ps < kBN ? ps : kBN;
       const int sl = lane % C::kSlices, pp = lane / C::kSlices;
       const bool mine = pp < kBN / box;
-      const uint32_t dst0 = sbase + sl * C::kSub + pp * box * 128;
-      int n = 0;  // key tiles, across pieces
+      const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kSub + pp * box * 128;
+      int slot = 0, round = 0, issued = 0;
       bool ok = true;
       do {
         const int h = walk.seg / walk.rt;
@@ -143,146 +173,211 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
           return w.p.num_pages;  // outside the map: the box arrives as zeros
         };
         int page = page_at(0);
-        for (int kt = 0; kt < walk.count; ++kt, ++n) {
+        for (int kt = 0; kt < walk.count; ++kt) {
           const int page_next = page_at(kt + 1);
-          const int s = n % C::kStages;
-          const uint32_t round = static_cast<uint32_t>(n / C::kStages);
           const unsigned bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
           const int in_page = ((walk.first + walk.kt + kt) * kBN + pp * box) % ps;
-          if (round > 0) ok = mbar_wait(bar(kBarKFree + s), (round - 1) & 1, abort_flag, w.status);
+          if (round > 0) ok = mbar_wait(bar(free + slot), (round - 1) & 1, abort_flag, w.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarKFull + s), bytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), bytes);
           __syncwarp();
-          if (page >= 0)
-            tma_load_4d(dst0 + C::kOffK + s * C::kTile, &tm_k, bar(kBarKFull + s), sl * 64, in_page, h, page);
-          if (round > 0) ok = mbar_wait(bar(kBarVFree + s), (round - 1) & 1, abort_flag, w.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) {
-            ++n;  // this tile's K is under way
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + s), bytes);
-          __syncwarp();
-          if (page >= 0)
-            tma_load_4d(dst0 + C::kOffV + s * C::kTile, &tm_v, bar(kBarVFull + s), sl * 64, in_page, h, page);
+          if (page >= 0) tma_load_4d(dst0 + slot * C::kTile, map, bar(full + slot), sl * 64, in_page, h, page);
+          ++issued;
           page = page_next;
+          if (++slot == stages) {
+            slot = 0;
+            ++round;
+          }
         }
       } while (ok && walk.next());
       if (*abort_flag && lane == 0) {
         // let copies already in flight land before the CTA exits (bounded)
         volatile int never = 0;
-        for (int x = max(0, n - C::kStages); x < n; ++x) {
-          mbar_wait(bar(kBarKFull + x % C::kStages), (x / C::kStages) & 1, &never, nullptr, 10000000ull);
-          mbar_wait(bar(kBarVFull + x % C::kStages), (x / C::kStages) & 1, &never, nullptr, 10000000ull);
-        }
+        for (int x = max(0, issued - stages); x < issued; ++x)
+          mbar_wait(bar(full + x % stages), (x / stages) & 1, &never, nullptr, 10000000ull);
       }
-    } else if (warp == kMma) {
+    } else if (work && warp < C::kMma + C::kLanes) {
+      // ------------------------------------------------------------- MMA
       if (lane == 0) {
+        const int a = warp - C::kMma;
         constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, 0);
         constexpr uint32_t idesc_o = idesc_f16_f32(kBM, D, 1);  // P and V in f16
-        int n = 0, piece = 0;
+        const uint32_t tS = tmem + C::kColS + 128 * a, tO = tmem + C::kColO + D * a;
+        const uint32_t qbase = sbase + C::kOffQ + a * C::kTile;
+        // turn x (counted across pieces): lane 1 waits for lane 0's turn x, lane 0 for lane 1's turn x - 1
+        auto wait_turn = [&](int x) -> bool {
+          if (C::kLanes == 1) return true;
+          if (a == 1) return mbar_wait_spin(bar(kBarTurn + 0), x & 1, abort_flag, w.status);
+          return x == 0 || mbar_wait_spin(bar(kBarTurn + 1), (x - 1) & 1, abort_flag, w.status);
+        };
+        auto end_turn = [&]() {
+          if (C::kLanes == 2) mbar_arrive(bar(kBarTurn + a));
+        };
+        // a tile's slot is free for reloading once this lane's products on it
+        // are done (a lane on its own tiles stands for the other one, too)
+        auto release = [&](int idx, bool ap) {
+          umma_commit(bar(idx));
+          if (ap) umma_commit(bar(idx));
+        };
+        int n0 = 0, mine = 0, piece = 0, turn = 0;  // key tiles, this lane's tiles: across pieces
         bool ok = true;
         do {
-          ok = mbar_wait(bar(kBarQFull), piece & 1, abort_flag, w.status);
-          for (int kt = 0; ok && kt < walk.count; ++kt, ++n) {
-            const int s = n % C::kStages;
-            const uint32_t ph = static_cast<uint32_t>(n / C::kStages) & 1u;
-            if (!(ok = mbar_wait_spin(bar(kBarKFull + s), ph, abort_flag, w.status))) break;
-            tc_fence_after();
-            const uint32_t kbase = sbase + C::kOffK + s * C::kTile;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kSub + (kk & 3) * 32;
-              umma_f16_ss(tmem, smem_desc_sw128(sbase + C::kOffQ + off, 16, 1024),
-                          smem_desc_sw128(kbase + off, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+          const bool ap = apart();
+          const int step = ap ? 2 : 1, kt0 = ap ? a : 0;
+          // one turn for the first S, then one for each of the tiles (of the lane that has more)
+          const int turns = 1 + (ap ? (walk.count + 1) / 2 : walk.count);
+          ok = mbar_wait(bar(kBarQFull + a), piece & 1, abort_flag, w.status);
+          // turn x: P V of the lane's tile x - 1 and S of its tile x
+          for (int x = 0; ok && x < turns; ++x, ++turn) {
+            const int kt = kt0 + (x - 1) * step;  // of P V
+            const bool pv = x > 0 && kt < walk.count, sn = kt + step < walk.count;
+            const int np = n0 + kt, ns = np + step;
+            const int vs = np % C::kVStages, ks = ns % C::kKStages;
+            if (pv) {
+              if (!(ok = mbar_wait_spin(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag, w.status))) break;
+              if (!(ok = mbar_wait_spin(bar(kBarPHalf + a), mine & 1, abort_flag, w.status))) break;
             }
-            umma_commit(bar(kBarSFull));
-            umma_commit(bar(kBarKFree + s));
-            const uint32_t vbase = sbase + C::kOffV + s * C::kTile;
-            auto issue_pv = [&](int kk0, int kk1) {
+            if (sn && !(ok = mbar_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status))) break;
+            if (!(ok = wait_turn(turn))) break;
+            tc_fence_after();
+            if (pv) {
+              const uint32_t vbase = sbase + C::kOffV + vs * C::kTile;
 #pragma unroll
-              for (int kk = kk0; kk < kk1; ++kk)
-                umma_f16_ts(tmem + C::kColO, tmem + kk * 8, smem_desc_sw128(vbase + kk * 16 * 128, C::kSub, 1024),
-                            idesc_o, (kt > 0 || kk > 0) ? 1u : 0u);
-            };
-            if (!(ok = mbar_wait_spin(bar(kBarVFull + s), ph, abort_flag, w.status))) break;
-            if (!(ok = mbar_wait_spin(bar(kBarPHalf), n & 1, abort_flag, w.status))) break;
-            tc_fence_after();
-            issue_pv(0, kBN / 32);
-            if (!(ok = mbar_wait_spin(bar(kBarPFull), n & 1, abort_flag, w.status))) break;
-            tc_fence_after();
-            issue_pv(kBN / 32, kBN / 16);
-            umma_commit(bar(kBarVFree + s));
-            if (kt + 1 == walk.count) umma_commit(bar(kBarODone));
+              for (int kk = 0; kk < kBN / 16; ++kk) {
+                if (kk == kBN / 32) {
+                  if (!(ok = mbar_wait_spin(bar(kBarPFull + a), mine & 1, abort_flag, w.status))) break;
+                  tc_fence_after();
+                }
+                umma_f16_ts(tO, tS + kk * 8, smem_desc_sw128(vbase + kk * 16 * 128, C::kSub, 1024), idesc_o,
+                            (x > 1 || kk > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              ++mine;
+            }
+            // S over the columns that these products read as P: the tensor core takes them in order
+            if (sn) {
+              const uint32_t kbase = sbase + C::kOffK + ks * C::kTile;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::kSub + (kk & 3) * 32;
+                umma_f16_ss(tS, smem_desc_sw128(qbase + off, 16, 1024), smem_desc_sw128(kbase + off, 16, 1024),
+                            idesc_s, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(bar(kBarSFull + a));
+            }
+            end_turn();
+            if (sn) release(kBarKFree + ks, ap);
+            if (pv) {
+              if (!sn) umma_commit(bar(kBarODone + a));
+              release(kBarVFree + vs, ap);
+            }
           }
+          n0 += walk.count;
           ++piece;
         } while (ok && walk.next());
         // every MMA issued above completes before TMEM is released
-        umma_commit(bar(kBarDrain));
+        umma_commit(bar(kBarDrain + a));
         volatile int never = 0;
-        mbar_wait(bar(kBarDrain), 0, &never, nullptr);
+        mbar_wait(bar(kBarDrain + a), 0, &never, nullptr);
       }
     }
   } else {
-    if constexpr (D != 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    const int row = threadIdx.x;  // 0..127, the TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tS = tmem + lane_base, tO = tmem + lane_base + C::kColO;
+    // ------------------------------------------------------------ softmax
+    if constexpr (C::kLanes == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int a = warp >> 2;            // the lane
+    const int row = threadIdx.x & 127;  // the TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + C::kColS + 128 * a, tO = tmem + lane_base + C::kColO + D * a;
     const float scale_log2 = w.scale * kLog2e;
-    int n = 0, piece = 0;
+    int n0 = 0, mine = 0, ends = 0;  // key tiles, this lane's tiles and its pieces with any: across pieces
     bool ok = true;
+    // The first round is a rehearsal: the code below comes a cache line at a
+    // time from L2 the first time that it runs (6 us for a tile's softmax,
+    // against 1.2 us later), which is over before the first S is there when it
+    // is spent on whatever TMEM holds while the work is laid out and K and Q
+    // are on their way.  Nothing of it is kept.
+    bool rehearsal = true;
+    int kt0 = 0, step = 1, count = 1, in_tile = 0, lim = INT_MAX, hi = INT_MAX, first = 0;
+    bool ap = false, valid = false, warp_valid = true;
+    // Sends for a piece's Q (16 bytes a copy, a row's copies next to each
+    // other, rows without a query zero): its arrival is waited for by land_q.
+    // The lane's last S of the piece before is done by then.
+    auto send_q = [&](const PagedWalk<kBN, C::kRows>& k) {
+      const int h = k.seg / k.rt;
+      const int tile_row = C::kLanes == 2 && k.tm <= kBM ? row : a * kBM + row;
+      const int r = (k.seg - h * k.rt) * k.tm + tile_row;
+      long long off = -1;
+      if (tile_row < k.tm && r < (k.it.t1 - k.it.t0) * gh) {
+        const int t = r / gh;
+        off = (k.it.t0 + t) * w.q_stride + static_cast<long long>(h * gh + r - t * gh) * D;
+      }
+      constexpr int kVecs = D / 8, kPer = 32 / kVecs;  // copies of a row, rows a step
+      const int c = lane % kVecs;
+#pragma unroll 4
+      for (int i = 0; i < kVecs; ++i) {
+        const int src = kPer > 0 ? i * kPer + lane / kVecs : i;
+        const long long o = __shfl_sync(0xffffffffu, off, src);
+        const int rr = (warp & 3) * 32 + src;
+        cp_async16(sbase + C::kOffQ + a * C::kTile + (c >> 3) * C::kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                   static_cast<const __nv_bfloat16*>(w.q) + (o < 0 ? 0 : o + 8 * c), o >= 0);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto land_q = [&]() {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQFull + a));
+    };
     do {
-      const int h = walk.seg / walk.rt, rt = walk.seg - h * walk.rt;
-      const int rows = (walk.it.t1 - walk.it.t0) * gh;
-      const int r = rt * walk.tm + row;
-      const bool valid = row < walk.tm && r < rows;
-      const bool warp_valid = __any_sync(0xffffffffu, valid);
-      // Q of the piece (the previous piece's last S is done: its SFull was waited for)
-      int lim = 0;
-      {
-        const __nv_bfloat16* q = nullptr;
+      if (!rehearsal) {
+        ap = apart();
+        step = ap ? 2 : 1;
+        kt0 = ap ? a : 0;
+        count = walk.count;
+        first = walk.first + walk.kt;
+        hi = walk.it.hi;
+        in_tile = ap ? row : a * kBM + row;
+        const int r = (walk.seg % walk.rt) * walk.tm + in_tile;
+        valid = in_tile < walk.tm && r < (walk.it.t1 - walk.it.t0) * gh;
+        warp_valid = __any_sync(0xffffffffu, valid);
+        lim = 0;
         if (valid) {
           const int t = walk.it.t0 + r / gh;
-          lim = min(walk.it.hi, paged_limit(w.p, paged_seq_of(w.p, t), t));
-          q = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride +
-              static_cast<long long>(h * gh + r % gh) * D;
+          lim = min(hi, paged_limit(w.p, paged_seq_of(w.p, t), t));
         }
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = valid ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(smem + C::kOffQ + (c >> 3) * C::kSub + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-              v;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQFull));
+        land_q();
       }
       float m_run = -INFINITY;  // maximum that the weights are taken against (log2 units)
       float l_run = 0.f;
-      for (int kt = 0; kt < walk.count; ++kt, ++n) {
-        const int k0 = (walk.first + walk.kt + kt) * kBN;
-        if (!(ok = mbar_wait(bar(kBarSFull), n & 1, abort_flag, w.status))) break;
-        tc_fence_after();
-        if (k0 + kBN > walk.it.hi) {
-          // slots behind the prefix may hold anything, NaN included, and 0 *
-          // NaN is NaN: V's rows there are zeroed (a thread a row)
-          const int s = n % C::kStages;
-          if (!(ok = mbar_wait(bar(kBarVFull + s), static_cast<uint32_t>(n / C::kStages) & 1u, abort_flag, w.status)))
-            break;
-          if (k0 + row >= walk.it.hi) {
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(smem + C::kOffV + s * C::kTile + (c >> 3) * C::kSub + row * 128 +
-                                        ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+      for (int kt = kt0; kt < count; kt += step) {
+        const int k0 = (first + kt) * kBN;
+        if (!rehearsal) {
+          if (!(ok = mbar_wait(bar(kBarSFull + a), mine & 1, abort_flag, w.status))) break;
+          ++mine;
+          tc_fence_after();
+          if (k0 + kBN > hi) {
+            // slots behind the prefix may hold anything, NaN included, and 0 *
+            // NaN is NaN: V's rows there are zeroed (a thread a row; lanes that share
+            // the tile write the same zeros)
+            const int n = n0 + kt, s = n % C::kVStages;
+            if (!(ok = mbar_wait(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag, w.status))) break;
+            if (k0 + row >= hi) {
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(smem + C::kOffV + s * C::kTile + (c >> 3) * C::kSub + row * 128 +
+                                          ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // before this warp's arrival on PHalf, which takes all four
           }
-          fence_proxy_async_smem();  // before this warp's arrival on PHalf, which takes all four
-        }
-        if (!warp_valid) {  // no row of this warp counts: its P may be anything
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(kBarPHalf));
-            mbar_arrive(bar(kBarPFull));
+          if (!warp_valid) {  // no row of this warp counts: its P may be anything
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar(kBarPHalf + a));
+              mbar_arrive(bar(kBarPFull + a));
+            }
+            continue;
           }
-          continue;
         }
         float s[kBN];
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -349,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
           }
         };
         exp_cols(0);
-        if (any && kt > 0) {
+        if (any && (kt > kt0 || rehearsal)) {
           // O is rescaled before this tile's products; the last tile's are
           // done, since this S was issued after them
           const uint64_t alpha2 = f2_pack(alpha, alpha);
@@ -378,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPHalf));
+        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPHalf + a));
         exp_cols(kBN / 2);
         {
           float a0, a1, b0, b1;
@@ -389,37 +484,55 @@ __global__ void __launch_bounds__(kThreads, PrefixCfg<D>::kCtas)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull));
+        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPFull + a));
       }
       if (!ok) break;
-      if (!(ok = mbar_wait(bar(kBarODone), piece & 1, abort_flag, w.status))) break;
-      tc_fence_after();
+      if (rehearsal) {
+        rehearsal = false;
+        __syncthreads();  // the schedule is there; what this round wrote to TMEM is behind tc_fence_before
+        if (!walk.init(&w.p, gh, w.prefix, sc)) break;
+        send_q(walk);
+        continue;
+      }
+      const long long part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg, walk.pm) + in_tile +
+                             (ap ? a * walk.tm : 0);  // lanes apart: lane 1's rows lie behind lane 0's
+      const bool more = walk.next();
+      if (more) send_q(walk);
+      const bool any_tile = kt0 < count;
+      if (any_tile) {
+        if (!(ok = mbar_wait(bar(kBarODone + a), ends & 1, abort_flag, w.status))) break;
+        ++ends;
+        tc_fence_after();
+      }
       if (warp_valid) {
-        const long long part = paged_part_row(blockIdx.x, kBM, walk.item_row, walk.seg, walk.tm) + row;
+        // a lane without a tile says so by its sum of 0
         if (valid) w.prefix.part_ml[part] = make_float2(m_run, l_run);
         float* dst = w.prefix.part_o + part * D;
+        if (any_tile) {
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          reg_dep32(o);
-          if (valid) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_dep32(o);
+            if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
           }
+          tc_fence_before();  // the next piece's P V overwrites O after this warp's next arrival
         }
-        tc_fence_before();  // the next piece's P V overwrites O after this warp's next arrival
       }
-      ++piece;
-    } while (walk.next());
+      n0 += count;
+      if (!more) break;
+    } while (true);
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == C::kMma) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <int D>
@@ -432,15 +545,11 @@ cudaError_t run(const PagedWork& w, cudaStream_t stream) {
   cudaError_t e =
       cudaFuncSetAttribute(paged_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  paged_prefix_kernel<D><<<w.prefix.ctas, kThreads, C::kSmemBytes, stream>>>(mk, mv, w);
+  paged_prefix_kernel<D><<<w.prefix.ctas, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, w);
   return cudaGetLastError();
 }
 
 }  // namespace
-
-int paged_prefix_ctas(int head_dim, int sms) {
-  return sms * (head_dim == 256 ? PrefixCfg<256>::kCtas : PrefixCfg<128>::kCtas);
-}
 
 cudaError_t launch_paged_prefix(const PagedWork& w, cudaStream_t stream) {
   switch (w.p.head_dim) {

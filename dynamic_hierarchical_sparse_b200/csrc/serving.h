@@ -87,10 +87,10 @@ cudaError_t launch_paged_attention(const PagedWork& w, int dtype, cudaStream_t s
 // TMA view of a 16-bit page array; one box is 64 columns of up to `tile` tokens of a page.
 CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16);
 
-// The prefixes' list on tcgen05 (bf16): tiles of 128 rows and 128 keys.
+// The prefixes' list on tcgen05 (bf16): key tiles of 128, row tiles of up to
+// 256 (128 for d 256), one CTA an SM.
 constexpr int kPrefixBN = 128;
-constexpr int kPrefixRows = 128;
-int paged_prefix_ctas(int head_dim, int sms);
+constexpr int paged_prefix_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 cudaError_t launch_paged_prefix(const PagedWork& w, cudaStream_t stream);
 
 }  // namespace dhsa

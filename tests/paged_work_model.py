@@ -9,14 +9,20 @@ def tile_rows(rows, most):
     return m
 
 
+def part_tile(tm, most):
+    """Rows of a segment's partials: two partials of small tiles where tiles reach 256 rows."""
+    return 2 * tm if most == 256 and tm <= 128 else tm
+
+
 def spans(items, hkv, bn, most):
-    """items: (rows, lo, hi).  Per item: (units, part rows, tile rows, row tiles, key tiles)."""
+    """items: (rows, lo, hi).  Per item: (units, part rows, partial rows of a segment, row tiles, key tiles)."""
     out = []
     for rows, lo, hi in items:
         tm = tile_rows(rows, most)
         rt = -(-rows // tm)
         nt = (hi + bn - 1) // bn - lo // bn if hi > lo and rows > 0 else 0
-        out.append((hkv * rt * nt, hkv * rt * tm, tm, rt, nt))
+        pm = part_tile(tm, most)
+        out.append((hkv * rt * nt, hkv * rt * pm, pm, rt, nt))
     return out
 
 

@@ -10,15 +10,15 @@ import pytest
 from tests import paged_work_model as M
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(100))
 def test_pieces_cover_and_partials_are_apart(seed):
     r = random.Random(seed)
-    bn, most = r.choice([(64, 64), (32, 16)])
+    bn, most = r.choice([(64, 64), (32, 16), (128, 256), (128, 128)])
     hkv, ctas = r.choice([1, 2, 3, 8]), r.choice([1, 7, 148, 296, 444])
     items = []
     for _ in range(r.randint(1, 30)):
         lo = r.choice([0, 0, r.randint(0, 3000)])
-        items.append((r.choice([0, 1, 4, 16, 17, 40, 64, 65, 500]), lo, max(lo, lo + r.randint(-100, 4000))))
+        items.append((r.choice([0, 1, 4, 16, 17, 40, 64, 65, 128, 129, 256, 257, 500]), lo, max(lo, lo + r.randint(-100, 4000))))
     got, sp, total = M.pieces(items, hkv, bn, most, ctas)
     rows_total = sum(s[1] for s in sp) + ctas * most
     taken, intervals = {}, []
@@ -35,11 +35,11 @@ def test_pieces_cover_and_partials_are_apart(seed):
     # the join's view
     unit = base = 0
     by = {(c, i, seg): row for c, i, seg, _, _, row, _ in got}
-    for i, (units, part, tm, rt, nt) in enumerate(sp):
+    for i, (units, part, pm, rt, nt) in enumerate(sp):
         for seg in range(hkv * rt if nt else 0):
             u0 = unit + seg * nt
             c0, c1 = M.owner(u0, total, ctas), M.owner(u0 + nt - 1, total, ctas)
-            first = c0 * most + base + seg * tm
+            first = c0 * most + base + seg * pm
             for c in range(c0, c1 + 1):
                 assert by[c, i, seg] == first + (c - c0) * most
                 assert any(taken[i, seg, x] == c for x in range(nt))
