@@ -116,6 +116,8 @@ PagedArgs paged_args(const dhsa_paged_cache* c, const dhsa_paged_batch* b) {
   a.uniform_q = b->num_seqs > 0 ? b->h_cu_q[1] : 0;
   for (int i = 1; i < b->num_seqs && a.uniform_q > 0; ++i)
     if (b->h_cu_q[i + 1] - b->h_cu_q[i] != a.uniform_q) a.uniform_q = 0;
+  a.by_uniform_q = FastDiv(a.uniform_q > 0 ? static_cast<uint32_t>(a.uniform_q) : 1u);
+  while ((1 << a.page_shift) < c->page_size) ++a.page_shift;
   return a;
 }
 
@@ -319,6 +321,7 @@ dhsa_status dhsa_paged_attention(const dhsa_paged_cache* cache, const dhsa_paged
   w.out_stride = ao.stride;
   w.lse = lse;
   w.num_q_heads = num_q_heads;
+  w.by_group = FastDiv(static_cast<uint32_t>(num_q_heads / cache->num_kv_heads));
   w.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(cache->head_dim));
   w.status = reinterpret_cast<uint32_t*>(ws);
   const int groups = w.p.num_groups;

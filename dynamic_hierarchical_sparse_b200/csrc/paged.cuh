@@ -54,7 +54,7 @@ __device__ __forceinline__ int paged_group_of(const PagedArgs& p, int b) {
 
 // The sequence that brings token t < total_q.
 __device__ __forceinline__ int paged_seq_of(const PagedArgs& p, int t) {
-  if (p.uniform_q > 0) return t / p.uniform_q;
+  if (p.uniform_q > 0) return p.by_uniform_q(t);
   int lo = 0, hi = p.num_seqs;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -91,19 +91,19 @@ __device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, int i) {
   return it;
 }
 
-// Rows of one segment's tile: a power of two from 16 to kMax that the item's
-// rows fill, so that few rows (one decode step of one sequence) take the form
-// in which all four warps split the keys, and many are worked on together.
+// log2 of the rows of one segment's tile: a power of two from 16 to kMax that
+// the item's rows fill, so that few rows (one decode step of one sequence) take
+// the form in which all four warps split the keys, and many are worked on together.
 template <int kMax>
-__host__ __device__ __forceinline__ int paged_tile_rows(int rows) {
-  int m = 16;
-  while (m < kMax && m < rows) m *= 2;
+__host__ __device__ __forceinline__ int paged_tile_shift(int rows) {
+  int m = 4;
+  while ((1 << m) < kMax && (1 << m) < rows) ++m;
   return m;
 }
 
 template <int kMaxRows>
-__host__ __device__ __forceinline__ int paged_part_tile(int tm) {
-  return kMaxRows == 256 && tm <= 128 ? 2 * tm : tm;
+__host__ __device__ __forceinline__ int paged_part_shift(int shift) {
+  return kMaxRows == 256 && shift < 8 ? shift + 1 : shift;
 }
 
 // An item's segments and key tiles.  Lists whose row tiles reach 256 (the
@@ -111,14 +111,14 @@ __host__ __device__ __forceinline__ int paged_part_tile(int tm) {
 template <int BN, int kMaxRows>
 struct PagedSpan {
   static constexpr int kMax = kMaxRows;
-  int rows, tm, rt, first, nt;  // rows; rows a tile, row tiles; first key tile, key tiles
-  int pm;                       // rows of a segment's partials
+  int rows, ts, rt, first, nt;  // rows; log2 rows a tile, row tiles; first key tile, key tiles
+  int ps;                       // log2 rows of a segment's partials
   PagedSpan() = default;
   __device__ __forceinline__ PagedSpan(const PagedItem& it, int group_heads) {
     rows = (it.t1 - it.t0) * group_heads;
-    tm = paged_tile_rows<kMaxRows>(rows);
-    rt = (rows + tm - 1) / tm;
-    pm = paged_part_tile<kMaxRows>(tm);
+    ts = paged_tile_shift<kMaxRows>(rows);
+    rt = (rows + (1 << ts) - 1) >> ts;
+    ps = paged_part_shift<kMaxRows>(ts);
     first = it.lo / BN;
     nt = it.hi > it.lo && rows > 0 ? (it.hi + BN - 1) / BN - first : 0;
   }
@@ -126,7 +126,7 @@ struct PagedSpan {
     return static_cast<long long>(num_kv_heads) * rt * nt;
   }
   __device__ __forceinline__ long long part_rows(int num_kv_heads) const {
-    return static_cast<long long>(num_kv_heads) * rt * pm;
+    return static_cast<long long>(num_kv_heads) * rt << ps;
   }
 };
 
@@ -152,8 +152,8 @@ __device__ __forceinline__ int paged_owner(long long unit, long long total, int 
 // Where CTA c's partial of a segment starts (rows): c steps by the largest
 // tile, a segment by its own rows, and along the list either c or the segment moves
 // on, so no two partials overlap.
-__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int pm) {
-  return static_cast<long long>(c) * max_rows + item_row + static_cast<long long>(seg) * pm;
+__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int ps) {
+  return static_cast<long long>(c) * max_rows + item_row + (static_cast<long long>(seg) << ps);
 }
 
 // Shared-memory words of the block-wide scan.
@@ -247,19 +247,23 @@ struct PagedWalk {
   int group_heads, end;
   int i;
   PagedItem it;
-  int tm, pm, rt, first, nt;
+  int ts, ps, rt, first, nt;
   long long item_row, left;
-  int seg, kt, count;  // current piece: segment, first key tile (of the item), tiles
+  int h, ri;      // current piece: KV head, row tile,
+  int kt, count;  // first key tile (of the item), tiles
 
   __device__ __forceinline__ void load() {
     it = paged_item(*p, i);
     const PagedSpan<BN, kMaxRows> sp(it, group_heads);
-    tm = sp.tm;
-    pm = sp.pm;
+    ts = sp.ts;
+    ps = sp.ps;
     rt = sp.rt;
     first = sp.first;
     nt = sp.nt;
   }
+  __device__ __forceinline__ int seg() const { return h * rt + ri; }
+  __device__ __forceinline__ int row0() const { return ri << ts; }  // the tile's first row
+  __device__ __forceinline__ int rows() const { return (it.t1 - it.t0) * group_heads; }
   // false: no work for this CTA
   __device__ __forceinline__ bool init(const PagedArgs* args, int gh, const PagedList& list, const PagedScan* sc) {
     p = args;
@@ -272,8 +276,10 @@ struct PagedWalk {
     item_row = sc->item_row;
     load();
     const long long off = u0 - sc->item_unit;
-    seg = static_cast<int>(paged_divide(off, nt));
-    kt = static_cast<int>(off - static_cast<long long>(seg) * nt);
+    const int s = static_cast<int>(paged_divide(off, nt));
+    kt = static_cast<int>(off - static_cast<long long>(s) * nt);
+    h = rt == 1 ? s : s / rt;
+    ri = s - h * rt;
     count = static_cast<int>(min(static_cast<long long>(nt - kt), left));
     return true;
   }
@@ -281,13 +287,16 @@ struct PagedWalk {
     left -= count;
     if (left <= 0) return false;
     kt = 0;
-    if (++seg == p->num_kv_heads * rt) {
-      seg = 0;
-      do {
-        item_row += static_cast<long long>(p->num_kv_heads) * rt * pm;
-        if (++i >= end) return false;
-        load();
-      } while (nt == 0);
+    if (++ri == rt) {
+      ri = 0;
+      if (++h == p->num_kv_heads) {
+        h = 0;
+        do {
+          item_row += static_cast<long long>(p->num_kv_heads) * rt << ps;
+          if (++i >= end) return false;
+          load();
+        } while (nt == 0);
+      }
     }
     count = static_cast<int>(min(static_cast<long long>(nt), left));
     return true;

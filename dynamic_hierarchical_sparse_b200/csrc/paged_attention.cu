@@ -122,9 +122,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wm = warp / WN, wn = warp % WN;
   const int gh = k.group_heads;
-  const int h = k.seg / k.rt, rt = k.seg - h * k.rt;
-  const int rows = (k.it.t1 - k.it.t0) * gh;
-  const int row0 = rt * k.tm;  // first row of the tile
+  const int h = k.h, rows = k.rows(), row0 = k.row0();
   const float scale_log2 = w.scale * kLog2e;
 
   // this thread's two rows: lane / 4 and + 8 of the warp's 16
@@ -136,10 +134,11 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     lim[e] = 0;
     qrow[e] = nullptr;
     if (r < rows) {
-      const int t = k.it.t0 + r / gh;
+      const int tr = w.by_group(r), t = k.it.t0 + tr;
       const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
       lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
-      qrow[e] = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride + static_cast<long long>(h * gh + r % gh) * D;
+      qrow[e] = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride +
+                static_cast<long long>((h - tr) * gh + r) * D;
     }
   }
   // the warp's smallest and largest limit over its valid rows
@@ -304,7 +303,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
     f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
   }
-  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg, k.pm);
+  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg(), k.ps);
   const int valid = min(rows - row0, WM * 16);
   if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
     const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
   ctx.phase = 0;
   PagedScan* sc = reinterpret_cast<PagedScan*>(smem + C::kOffScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  const int gh = w.by_group.d;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full(ctx, s), 1);
@@ -390,22 +389,22 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 
   if (warp == kProducer) {
     // a lane for each box of a tile: (page part, 64-column slice, K or V)
-    const int ps = w.p.page_size;
+    const int ps = w.p.page_size, psh = w.p.page_shift;
     const int box = ps < kBN ? ps : kBN;
     const int kv = lane & 1, sl = (lane >> 1) % C::kSlices, pp = (lane >> 1) / C::kSlices;
-    const bool mine = pp < kBN / box;
+    const bool mine = pp * box < kBN;
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const uint32_t dst0 = ctx.sbase + kv * C::kTileBytes + sl * (kBN * 128) + pp * box * 128;
     int issued = 0;
     bool ok = true;
     do {
-      const int h = walk.seg / walk.rt;
+      const int h = walk.h;
       const int* table = w.p.block_table + static_cast<long long>(walk.it.row) * w.p.table_stride;
       // the page of this lane's part of a tile, -1 where the item has no key in it
       auto page_at = [&](int kt) -> int {
         const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
         if (kt >= walk.count || !mine || key >= walk.it.hi || key + box <= walk.it.lo) return -1;
-        const int pg = table[key / ps];
+        const int pg = table[key >> psh];
         if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) return pg;
         report(w.status, kDevCheck);
         return w.p.num_pages;  // outside the map: the box arrives as zeros
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
         __syncwarp();
         if (page >= 0) {
           const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
-          tma_load_4d(dst0 + s * 2 * C::kTileBytes, map, bar_full(ctx, s), sl * 64, key % ps, h, page);
+          tma_load_4d(dst0 + s * 2 * C::kTileBytes, map, bar_full(ctx, s), sl * 64, key & (ps - 1), h, page);
         }
         ++issued;
         page = page_next;
@@ -441,9 +440,9 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
   } else {
     bool ok;
     do {
-      if (walk.tm == 16) {
+      if (walk.ts == 4) {
         ok = mma_piece<D, 1, 4>(w, walk, ctx);
-      } else if (walk.tm == 32) {
+      } else if (walk.ts == 5) {
         ok = mma_piece<D, 2, 2>(w, walk, ctx);
       } else {
         ok = mma_piece<D, 4, 1>(w, walk, ctx);
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(kFThreads)
   float* ps = reinterpret_cast<float*>(smem_raw + C::kOffP);  // [warp][key][4 rows]
   PagedScan* sc = reinterpret_cast<PagedScan*>(smem_raw + C::kOffScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  const int gh = w.by_group.d;
   paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, w.list, sc, w.status);
   __syncthreads();
   let_next_start();
@@ -486,8 +485,7 @@ __global__ void __launch_bounds__(kFThreads)
   if (!k.init(&w.p, gh, w.list, sc)) return;
   const float scale_log2 = w.scale * kLog2e;
   do {
-    const int h = k.seg / k.rt, rt = k.seg - h * k.rt;
-    const int rows = (k.it.t1 - k.it.t0) * gh, row0 = rt * k.tm;
+    const int h = k.h, rows = k.rows(), row0 = k.row0();
     const int* table = w.p.block_table + static_cast<long long>(k.it.row) * w.p.table_stride;
     auto fetch = [&](int kt) {
       const int buf = kt & 1;
@@ -498,9 +496,9 @@ __global__ void __launch_bounds__(kFThreads)
         bool take = key >= k.it.lo && key < k.it.hi;
         long long off = 0;
         if (take) {
-          const int pg = table[key / w.p.page_size];
+          const int pg = table[key >> w.p.page_shift];
           if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) {
-            off = pg * w.p.page_stride + (static_cast<long long>(h) * w.p.page_size + key % w.p.page_size) * D + 4 * c;
+            off = pg * w.p.page_stride + (static_cast<long long>(h) * w.p.page_size + (key & (w.p.page_size - 1))) * D + 4 * c;
           } else {
             take = false;  // taken as zeros
             report(w.status, kDevCheck);
@@ -518,9 +516,9 @@ __global__ void __launch_bounds__(kFThreads)
       const int r = row0 + x / (D / 4), c = x % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
-        const int t = k.it.t0 + r / gh;
-        v = *reinterpret_cast<const float4*>(static_cast<const float*>(w.q) + t * w.q_stride +
-                                             static_cast<long long>(h * gh + r % gh) * D + 4 * c);
+        const int tr = w.by_group(r);
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(w.q) + (k.it.t0 + tr) * w.q_stride +
+                                             static_cast<long long>((h - tr) * gh + r) * D + 4 * c);
       }
       *reinterpret_cast<float4*>(qs + (x / (D / 4)) * D + 4 * c) = v;
     }
@@ -534,7 +532,7 @@ __global__ void __launch_bounds__(kFThreads)
       const int r = row0 + warp * 4 + e;
       lim[e] = 0;
       if (r < rows) {
-        const int t = k.it.t0 + r / gh;
+        const int t = k.it.t0 + w.by_group(r);
         const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
         lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
       }
@@ -595,7 +593,7 @@ __global__ void __launch_bounds__(kFThreads)
       }
       __syncthreads();  // the buffer is free for the tile after next
     }
-    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg, k.pm);
+    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ps);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float sum = l[e];
@@ -620,24 +618,24 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   constexpr int kCols = D / 32;
   const int t = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  const int gh = w.by_group.d;
   const int b = paged_seq_of(w.p, t);
   T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
   // a row's partials of one item: rows at + j * kStep for j < count
   struct Place {
-    int seg, nt, tm, pm, in_tile, j, n;  // segment, its key tiles, tile and partial rows, row in the tile; item, items
+    int seg, nt, ts, ps, in_tile, j, n;  // segment, its key tiles, log2 tile and partial rows, row in the tile; item, items
   };
   auto place = [&](auto span, const PagedList& l, int i) -> Place {
     using Span = decltype(span);
     const PagedItem it = paged_item(w.p, i);
     const Span sp(it, gh);
-    const int r = (t - it.t0) * gh + h % gh;
-    return Place{(h / gh) * sp.rt + r / sp.tm, sp.nt, sp.tm, sp.pm, r % sp.tm, i - l.begin, l.end - l.begin};
+    const int g = w.by_group(h), r = (t - it.t0 - g) * gh + h;
+    return Place{g * sp.rt + (r >> sp.ts), sp.nt, sp.ts, sp.ps, r & ((1 << sp.ts) - 1), i - l.begin, l.end - l.begin};
   };
   const bool own_list = w.prefix.end > 0;
   const int limit = paged_limit(w.p, b, t);
   constexpr int kPrefixRows = paged_prefix_rows(D);
-  Place pp{0, 0, 1, 1, 0, 0, 0};
+  Place pp{0, 0, 0, 0, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
     pp = own_list ? place(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
@@ -656,15 +654,15 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const long long row = l.items[p.n + 1 + p.j];
     const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + p.nt - 1, total, l.ctas);
     count = c1 - c0 + 1;
-    return paged_part_row(c0, step, row, p.seg, p.pm) + p.in_tile;
+    return paged_part_row(c0, step, row, p.seg, p.ps) + p.in_tile;
   };
   const PagedList& pl = own_list ? w.prefix : w.list;
   const int pstep = own_list ? kPrefixRows : kMax;
   int pcount, ocount;
   const long long pfirst = first_row(pp, pl, pstep, pcount);
   const long long ofirst = first_row(po, w.list, kMax, ocount);
-  // a prefix's partials: one a CTA, or two (rows tm apart) where its lanes took turns
-  const int halves = pp.pm > pp.tm ? 1 : 0;
+  // a prefix's partials: one a CTA, or two (a tile apart) where its lanes took turns
+  const int halves = pp.ps - pp.ts;
   pcount <<= halves;
   const int all = pcount + ocount;
   float m = -INFINITY, sum = 0.f, acc[kCols];
@@ -682,7 +680,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
       if (j < all) {
         const bool pre = j < pcount;
-        const long long r = pre ? pfirst + static_cast<long long>(j >> halves) * pstep + (halves & j) * pp.tm
+        const long long r = pre ? pfirst + static_cast<long long>(j >> halves) * pstep + ((halves & j) << pp.ts)
                                 : ofirst + static_cast<long long>(j - pcount) * kMax;
         ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
         const float* o = (pre ? pl.part_o : w.list.part_o) + r * D;
@@ -832,17 +830,19 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
   PagedShape s{};
   const int gh = num_q_heads / p.num_kv_heads;
   const bool bf16 = dtype == DHSA_BF16;
-  auto padded = [](long long r, int tm) { return (r + tm - 1) / tm * tm; };
+  // rows padded to tiles of 2^ts, each tile's partials of 2^ps rows
+  auto padded = [](long long r, int ts, int ps) { return (r + (1 << ts) - 1) >> ts << ps; };
   auto list_rows = [&](long long r) {
-    return padded(r, bf16 ? paged_tile_rows<kMaxRows>(static_cast<int>(r)) : kFRows);
+    const int ts = bf16 ? paged_tile_shift<kMaxRows>(static_cast<int>(r)) : paged_tile_shift<kFRows>(static_cast<int>(r));
+    return padded(r, ts, ts);
   };
   const bool wide = paged_prefix_rows(p.head_dim) == 256;
   long long most = 0, prefix = 0, list = 0, groups_in_list = 0;
   for (int g = 0; g < p.num_groups; ++g) {
     const long long r = static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
     most = r > most ? r : most;
-    const int tm = wide ? paged_tile_rows<256>(static_cast<int>(r)) : paged_tile_rows<128>(static_cast<int>(r));
-    prefix += (r + tm - 1) / tm * (wide ? paged_part_tile<256>(tm) : tm);
+    const int ts = wide ? paged_tile_shift<256>(static_cast<int>(r)) : paged_tile_shift<128>(static_cast<int>(r));
+    prefix += padded(r, ts, wide ? paged_part_shift<256>(ts) : ts);
     groups_in_list += list_rows(r);
   }
   for (int b = 0; b < p.num_seqs; ++b) list += list_rows(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   PagedScan* sc = reinterpret_cast<PagedScan*>(smem + C::kOffScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.num_q_heads / w.p.num_kv_heads;
+  const int gh = w.by_group.d;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4; ++s) {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   PagedWalk<kBN, C::kRows> walk{};
   // Two lanes on one set of rows take every other key tile of a piece
   // (`apart`): lane a's tiles are a, a + 2, ...; otherwise every one.
-  auto apart = [&]() -> bool { return C::kLanes == 2 && walk.tm <= kBM; };
+  auto apart = [&]() -> bool { return C::kLanes == 2 && walk.ts < 8; };
 
   if (warp >= C::kProducer) {
     // 8 warps x 224 + 4 x 56 registers = the launch's 12 x 168
@@ -154,20 +154,20 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       const CUtensorMap* map = is_k ? &tm_k : &tm_v;
       const int full = is_k ? kBarKFull : kBarVFull, free = is_k ? kBarKFree : kBarVFree;
       const int stages = is_k ? C::kKStages : C::kVStages;
-      const int ps = w.p.page_size;
+      const int ps = w.p.page_size, psh = w.p.page_shift;
       const int box = ps < kBN ? ps : kBN;
       const int sl = lane % C::kSlices, pp = lane / C::kSlices;
-      const bool mine = pp < kBN / box;
+      const bool mine = pp * box < kBN;
       const uint32_t dst0 = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kSub + pp * box * 128;
       int slot = 0, round = 0, issued = 0;
       bool ok = true;
       do {
-        const int h = walk.seg / walk.rt;
+        const int h = walk.h;
         const int* table = w.p.block_table + static_cast<long long>(walk.it.row) * w.p.table_stride;
         auto page_at = [&](int kt) -> int {
           const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
           if (kt >= walk.count || !mine || key >= walk.it.hi) return -1;
-          const int pg = table[key / ps];
+          const int pg = table[key >> psh];
           if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) return pg;
           report(w.status, kDevCheck);
           return w.p.num_pages;  // outside the map: the box arrives as zeros
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         for (int kt = 0; kt < walk.count; ++kt) {
           const int page_next = page_at(kt + 1);
           const unsigned bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
-          const int in_page = ((walk.first + walk.kt + kt) * kBN + pp * box) % ps;
+          const int in_page = ((walk.first + walk.kt + kt) * kBN + pp * box) & (ps - 1);
           if (round > 0) ok = mbar_wait(bar(free + slot), (round - 1) & 1, abort_flag, w.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), bytes);
@@ -303,13 +303,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     // other, rows without a query zero): its arrival is waited for by land_q.
     // The lane's last S of the piece before is done by then.
     auto send_q = [&](const PagedWalk<kBN, C::kRows>& k) {
-      const int h = k.seg / k.rt;
-      const int tile_row = C::kLanes == 2 && k.tm <= kBM ? row : a * kBM + row;
-      const int r = (k.seg - h * k.rt) * k.tm + tile_row;
+      const int tile_row = C::kLanes == 2 && k.ts < 8 ? row : a * kBM + row;
+      const int r = k.row0() + tile_row;
       long long off = -1;
-      if (tile_row < k.tm && r < (k.it.t1 - k.it.t0) * gh) {
-        const int t = r / gh;
-        off = (k.it.t0 + t) * w.q_stride + static_cast<long long>(h * gh + r - t * gh) * D;
+      if (tile_row >> k.ts == 0 && r < k.rows()) {
+        const int tr = w.by_group(r);
+        off = (k.it.t0 + tr) * w.q_stride + static_cast<long long>((k.h - tr) * gh + r) * D;
       }
       constexpr int kVecs = D / 8, kPer = 32 / kVecs;  // copies of a row, rows a step
       const int c = lane % kVecs;
@@ -338,12 +337,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         first = walk.first + walk.kt;
         hi = walk.it.hi;
         in_tile = ap ? row : a * kBM + row;
-        const int r = (walk.seg % walk.rt) * walk.tm + in_tile;
-        valid = in_tile < walk.tm && r < (walk.it.t1 - walk.it.t0) * gh;
+        const int r = walk.row0() + in_tile;
+        valid = in_tile >> walk.ts == 0 && r < walk.rows();
         warp_valid = __any_sync(0xffffffffu, valid);
         lim = 0;
         if (valid) {
-          const int t = walk.it.t0 + r / gh;
+          const int t = walk.it.t0 + w.by_group(r);
           lim = min(hi, paged_limit(w.p, paged_seq_of(w.p, t), t));
         }
         land_q();
@@ -494,8 +493,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         send_q(walk);
         continue;
       }
-      const long long part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg, walk.pm) + in_tile +
-                             (ap ? a * walk.tm : 0);  // lanes apart: lane 1's rows lie behind lane 0's
+      const long long part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ps) + in_tile +
+                             (ap ? a << walk.ts : 0);  // lanes apart: lane 1's rows lie behind lane 0's
       const bool more = walk.next();
       if (more) send_q(walk);
       const bool any_tile = kt0 < count;

@@ -11,6 +11,24 @@
 
 namespace dhsa {
 
+// n / d for 0 <= n < 2^31 by a product and a shift (a division by a number that
+// is not known when compiling takes some forty instructions, which the first
+// pass over a kernel's code, the whole of a short call, pays for in fetching).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by) {
+    shift = 0;
+    while ((1u << shift) < by) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - by) << 32) / by + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+#endif
+};
+
 // A packed [T, H, d] operand with its token stride resolved (elements).
 struct TokensArg {
   void* data;
@@ -31,6 +49,8 @@ struct PagedArgs {
   const int* prefix_lens;
   int total_q;    // cu_q[B]
   int uniform_q;  // n when every sequence brings n >= 1 tokens (the owner of token t is t / n), else 0
+  FastDiv by_uniform_q;
+  int page_shift;  // log2(page_size)
 };
 
 // Rotary positions of q and k (either may be absent: data null).
@@ -67,6 +87,7 @@ struct PagedWork {
   long long out_stride;
   float* lse;  // may be null
   int num_q_heads;
+  FastDiv by_group;  // by Hq / Hkv
   float scale;
   PagedList prefix;  // the groups, where they are a list of their own; else empty
   PagedList list;    // the sequences, and the groups where `prefix` is empty

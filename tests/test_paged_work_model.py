@@ -44,3 +44,19 @@ def test_pieces_cover_and_partials_are_apart(seed):
                 assert by[c, i, seg] == first + (c - c0) * most
                 assert any(taken[i, seg, x] == c for x in range(nt))
         unit, base = unit + units, base + part
+
+
+def test_division_by_a_product():
+    """FastDiv of csrc/serving.h: exact for every 31-bit number, at the ends and borders of each divisor."""
+    r = random.Random(0)
+    for d in list(range(1, 3000)) + [2 ** i + j for i in range(12, 31) for j in (-1, 0, 1)] + [2 ** 31 - 1]:
+        shift = 0
+        while (1 << shift) < d:
+            shift += 1
+        mul = (((1 << shift) - d) << 32) // d + 1
+        assert mul < 2 ** 32
+        top = 2 ** 31 - 1
+        ns = [0, 1, d - 1, d, d + 1, top, top - 1, top // d * d, top // d * d - 1] + [r.randint(0, top) for _ in range(20)]
+        for n in ns:
+            if 0 <= n <= top:
+                assert (((n * mul) >> 32) + n) < 2 ** 32 and (((n * mul) >> 32) + n) >> shift == n // d, (n, d)
