@@ -137,7 +137,7 @@ dhsa_status attention_layout(const dhsa_paged_cache* c, const dhsa_paged_batch* 
     const size_t rows = static_cast<size_t>(x == 0 ? L->shape.prefix_rows : L->shape.list_rows);
     const size_t n = static_cast<size_t>(x == 0 ? L->shape.prefix_items : L->shape.list_items);
     L->items[x] = at;
-    at += align_up((2 * n + 1) * sizeof(long long));
+    at += align_up((2 * n + 2) * sizeof(long long));
     L->ml[x] = at;
     at += align_up(rows * sizeof(float2));
     L->o[x] = at;

@@ -101,143 +101,176 @@ __host__ __device__ __forceinline__ int paged_tile_shift(int rows) {
   return m;
 }
 
-template <int kMaxRows>
-__host__ __device__ __forceinline__ int paged_part_shift(int shift) {
-  return kMaxRows == 256 && shift < 8 ? shift + 1 : shift;
-}
-
-// An item's segments and key tiles.  Lists whose row tiles reach 256 (the
-// prefixes' own, for d 64 and 128) leave two partials of tiles of up to 128 rows.
+// An item's segments and key tiles.
 template <int BN, int kMaxRows>
 struct PagedSpan {
   static constexpr int kMax = kMaxRows;
   int rows, ts, rt, first, nt;  // rows; log2 rows a tile, row tiles; first key tile, key tiles
-  int ps;                       // log2 rows of a segment's partials
   PagedSpan() = default;
   __device__ __forceinline__ PagedSpan(const PagedItem& it, int group_heads) {
     rows = (it.t1 - it.t0) * group_heads;
     ts = paged_tile_shift<kMaxRows>(rows);
     rt = (rows + (1 << ts) - 1) >> ts;
-    ps = paged_part_shift<kMaxRows>(ts);
     first = it.lo / BN;
     nt = it.hi > it.lo && rows > 0 ? (it.hi + BN - 1) / BN - first : 0;
   }
-  __device__ __forceinline__ long long units(int num_kv_heads) const {
-    return static_cast<long long>(num_kv_heads) * rt * nt;
-  }
-  __device__ __forceinline__ long long part_rows(int num_kv_heads) const {
-    return static_cast<long long>(num_kv_heads) * rt << ps;
-  }
 };
 
-// First unit (key tile of the whole list) of CTA c, and the CTA that holds a
-// unit.  With fewer units than CTAs the first `total` CTAs take one each, so
-// every CTA between the first and the last owner of a segment has a partial of it.
-__device__ __forceinline__ int paged_ctas(long long total, int ctas) {
-  return static_cast<int>(min(total, static_cast<long long>(ctas)));
-}
 // (Products within 32 bits, the usual case, divide several times faster.)
 __device__ __forceinline__ long long paged_divide(long long a, long long b) {
   if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
-__device__ __forceinline__ long long paged_first_unit(long long c, long long total, int ctas) {
-  const int n = paged_ctas(total, ctas);
-  return c < n ? paged_divide(c * total, n) : total;
-}
-__device__ __forceinline__ int paged_owner(long long unit, long long total, int ctas) {
-  return static_cast<int>(paged_divide((unit + 1) * paged_ctas(total, ctas) - 1, total));
-}
+
+// How a list's key tiles (units) are cut among the CTAs.  chunk 0: evenly,
+// wherever that falls; with fewer units than CTAs the first `total` CTAs take
+// one each, so every CTA between the first and the last owner of a segment has
+// a partial of it.  chunk > 0: every segment counts as a whole number of chunks,
+// a CTA takes one chunk, and none has two segments.
+struct PagedCut {
+  long long total;
+  int chunk, ctas;
+  __device__ __forceinline__ int used() const { return static_cast<int>(min(total, static_cast<long long>(ctas))); }
+  __device__ __forceinline__ int padded(int nt) const {
+    return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt;
+  }
+  __device__ __forceinline__ long long first(long long c) const {  // the first unit of CTA c
+    if (chunk > 0) return min(c * chunk, total);
+    const int n = used();
+    return c < n ? paged_divide(c * total, n) : total;
+  }
+  __device__ __forceinline__ int owner(long long unit) const {  // the CTA that holds a unit
+    return static_cast<int>(chunk > 0 ? paged_divide(unit, chunk) : paged_divide((unit + 1) * used() - 1, total));
+  }
+};
 
 // Where CTA c's partial of a segment starts (rows): c steps by the largest
 // tile, a segment by its own rows, and along the list either c or the segment moves
 // on, so no two partials overlap.
-__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int ps) {
-  return static_cast<long long>(c) * max_rows + item_row + (static_cast<long long>(seg) << ps);
+__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int ts) {
+  return static_cast<long long>(c) * max_rows + item_row + (static_cast<long long>(seg) << ts);
 }
 
 // Shared-memory words of the block-wide scan.
 struct PagedScan {
-  long long warp_units[32], warp_rows[32];
-  long long total, item_unit, item_row;
+  long long warp_units[8], warp_rows[8];
+  int warp_segs[8];
+  PagedCut cut;
+  long long item_unit, item_row;
+  PagedItem it;
   int item;
 };
 
 // Every CTA counts the units of all items (each thread a run of them) and finds
 // the item that holds its first unit.  CTA 0 writes the items' first units and
-// rows for the join.  Called by the CTA's last kThreads threads, which meet at
-// barrier 1; the result is for the whole CTA after its next __syncthreads.
-template <int BN, int kMaxRows, int kThreads>
+// rows, and the cut, for the join.  kSnap > 0: where the segments are fewer than
+// half of the CTAs, they are cut into chunks, unless the longest share then is
+// more than kSnap units (what a second piece costs a CTA) above the even one.
+// Called by the CTA's last kThreads threads, which meet at barrier 1; the result
+// is for the whole CTA after its next __syncthreads.
+template <int BN, int kMaxRows, int kThreads, int kSnap>
 __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_heads, const PagedList& list,
                                                PagedScan* sc, uint32_t* status) {
   const int n = list.end - list.begin;
   const int per = (n + kThreads - 1) / kThreads;
   const int thread = threadIdx.x - (blockDim.x - kThreads);
   const int i0 = min(thread * per, n), i1 = min(i0 + per, n);
-  long long units = 0, rows = 0;
-  bool bad = false;
-  for (int i = i0; i < i1; ++i) {
-    const PagedItem it = paged_item(p, list.begin + i);
-    const PagedSpan<BN, kMaxRows> sp(it, group_heads);
-    units += sp.units(p.num_kv_heads);
-    rows += sp.part_rows(p.num_kv_heads);
-    if (blockIdx.x == 0) {
-      const int g = list.begin + i;
-      if (g < p.num_groups) {
-        bad |= it.t1 > it.t0 && p.prefix_lens[g] != paged_clamp_len(p, p.prefix_lens[g]);
-      } else {
-        bad |= p.kv_lens[g - p.num_groups] != it.hi;
-      }
-    }
-  }
-  if (bad) report(status, kDevCheck);
   const int lane = thread & 31, warp = thread >> 5;
-  long long iu = units, ir = rows;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
-    if (lane >= o) {
-      iu += u;
-      ir += r;
-    }
-  }
-  if (lane == 31) {
-    sc->warp_units[warp] = iu;
-    sc->warp_rows[warp] = ir;
-  }
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-  long long base_u = iu - units, base_r = ir - rows, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const long long u = sc->warp_units[w];
-    if (w < warp) {
-      base_u += u;
-      base_r += sc->warp_rows[w];
-    }
-    total += u;
-  }
-  const long long mine = paged_first_unit(blockIdx.x, total, gridDim.x);
-  if (thread == 0) sc->total = total;
-  const bool find = units > 0 && base_u <= mine && mine < base_u + units;
-  if (find || blockIdx.x == 0) {
-    long long u = base_u, r = base_r;
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
+  PagedCut cut{0, 0, static_cast<int>(gridDim.x)};
+  long long base_u = 0, base_r = 0;
+  // rounds (one body, so that its code comes in once): the plain count with
+  // its segments (kSnap), the padded count, then the finding of this CTA's item
+#pragma unroll 1
+  for (int round = kSnap > 0 ? 0 : 1; round < 3; ++round) {
+    const bool find = round == 2;
+    const long long mine = find ? cut.first(blockIdx.x) : 0;
+    long long units = base_u, rows = base_r;
+    if (!find) units = rows = 0;
+    int segs = 0;
+    bool bad = false;
     for (int i = i0; i < i1; ++i) {
       const PagedItem it = paged_item(p, list.begin + i);
       const PagedSpan<BN, kMaxRows> sp(it, group_heads);
-      const long long du = sp.units(p.num_kv_heads);
-      if (du > 0 && u <= mine && mine < u + du) {
-        sc->item = list.begin + i;
-        sc->item_unit = u;
-        sc->item_row = r;
+      const int tiles = p.num_kv_heads * sp.rt;
+      const long long du = static_cast<long long>(tiles) * cut.padded(sp.nt);
+      const long long dr = static_cast<long long>(tiles) << sp.ts;
+      if (find) {
+        if (du > 0 && units <= mine && mine < units + du) {
+          sc->item = list.begin + i;
+          sc->it = it;
+          sc->item_unit = units;
+          sc->item_row = rows;
+        }
+        if (blockIdx.x == 0) {
+          list.items[i] = units;
+          list.items[n + 2 + i] = rows;
+        }
+      } else if (blockIdx.x == 0 && round == 1) {
+        const int g = list.begin + i;
+        if (g < p.num_groups) {
+          bad |= it.t1 > it.t0 && p.prefix_lens[g] != paged_clamp_len(p, p.prefix_lens[g]);
+        } else {
+          bad |= p.kv_lens[g - p.num_groups] != it.hi;
+        }
       }
-      if (blockIdx.x == 0) {
-        list.items[i] = u;
-        list.items[n + 1 + i] = r;
+      units += du;
+      rows += dr;
+      segs += sp.nt > 0 ? tiles : 0;
+    }
+    if (find) break;
+    if (bad) report(status, kDevCheck);
+    long long iu = units, ir = rows;
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      const long long u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
+      if (lane >= o) {
+        iu += u;
+        ir += r;
       }
-      u += du;
-      r += sp.part_rows(p.num_kv_heads);
+    }
+    if (kSnap > 0 && round == 0) segs = __reduce_add_sync(0xffffffffu, segs);
+    if (lane == 31) {
+      sc->warp_units[warp] = iu;
+      sc->warp_rows[warp] = ir;
+      sc->warp_segs[warp] = segs;
+    }
+    meet();
+    base_u = iu - units;
+    base_r = ir - rows;
+    cut.total = 0;
+    segs = 0;
+#pragma unroll 1
+    for (int x = 0; x < kThreads / 32; ++x) {
+      const long long u = sc->warp_units[x];
+      if (x < warp) {
+        base_u += u;
+        base_r += sc->warp_rows[x];
+      }
+      cut.total += u;
+      segs += sc->warp_segs[x];
+    }
+    if (kSnap > 0 && round == 0) {
+      if (2 * segs < cut.ctas && cut.total > 0) {
+        const long long spare = cut.ctas - segs;
+        const long long chunk = paged_divide(cut.total + spare - 1, spare);
+        if (chunk <= paged_divide(cut.total, cut.ctas) + kSnap) cut.chunk = static_cast<int>(chunk);
+      }
+      meet();  // the words above are read before the next round writes them
+    }
+    // threads without the first unit have no more to do (CTA 0's write the items)
+    if (round == 1) {
+      if (thread == 0) {
+        sc->cut = cut;
+        if (blockIdx.x == 0) {
+          list.items[n] = cut.total;
+          list.items[n + 1] = cut.chunk;
+        }
+      }
+      const long long first = cut.first(blockIdx.x);
+      if (blockIdx.x != 0 && !(units > 0 && base_u <= first && first < base_u + units)) break;
     }
   }
-  if (blockIdx.x == 0 && thread == 0) list.items[n] = total;
 }
 
 // A CTA's walk over its pieces: consecutive key tiles of one segment each.
@@ -245,18 +278,17 @@ template <int BN, int kMaxRows>
 struct PagedWalk {
   const PagedArgs* p;
   int group_heads, end;
+  bool one;  // one piece a CTA
   int i;
   PagedItem it;
-  int ts, ps, rt, first, nt;
+  int ts, rt, first, nt;
   long long item_row, left;
   int h, ri;      // current piece: KV head, row tile,
   int kt, count;  // first key tile (of the item), tiles
 
-  __device__ __forceinline__ void load() {
-    it = paged_item(*p, i);
+  __device__ __forceinline__ void measure() {
     const PagedSpan<BN, kMaxRows> sp(it, group_heads);
     ts = sp.ts;
-    ps = sp.ps;
     rt = sp.rt;
     first = sp.first;
     nt = sp.nt;
@@ -269,15 +301,19 @@ struct PagedWalk {
     p = args;
     group_heads = gh;
     end = list.end;
-    const long long u0 = paged_first_unit(blockIdx.x, sc->total, gridDim.x);
-    left = paged_first_unit(blockIdx.x + 1, sc->total, gridDim.x) - u0;
+    const PagedCut& cut = sc->cut;
+    const long long u0 = cut.first(blockIdx.x);
+    left = cut.first(blockIdx.x + 1) - u0;
     if (left <= 0) return false;
+    one = cut.chunk > 0;
     i = sc->item;
+    it = sc->it;
     item_row = sc->item_row;
-    load();
+    measure();
     const long long off = u0 - sc->item_unit;
-    const int s = static_cast<int>(paged_divide(off, nt));
-    kt = static_cast<int>(off - static_cast<long long>(s) * nt);
+    const int ntp = cut.padded(nt);
+    const int s = static_cast<int>(paged_divide(off, ntp));
+    kt = static_cast<int>(off - static_cast<long long>(s) * ntp);
     h = rt == 1 ? s : s / rt;
     ri = s - h * rt;
     count = static_cast<int>(min(static_cast<long long>(nt - kt), left));
@@ -285,16 +321,17 @@ struct PagedWalk {
   }
   __device__ __forceinline__ bool next() {
     left -= count;
-    if (left <= 0) return false;
+    if (one || left <= 0) return false;
     kt = 0;
     if (++ri == rt) {
       ri = 0;
       if (++h == p->num_kv_heads) {
         h = 0;
         do {
-          item_row += static_cast<long long>(p->num_kv_heads) * rt << ps;
+          item_row += static_cast<long long>(p->num_kv_heads) * rt << ts;
           if (++i >= end) return false;
-          load();
+          it = paged_item(*p, i);
+          measure();
         } while (nt == 0);
       }
     }

@@ -303,7 +303,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
     f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
   }
-  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg(), k.ps);
+  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg(), k.ts);
   const int valid = min(rows - row0, WM * 16);
   if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
     const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  paged_schedule<kBN, kMaxRows, kMmaThreads>(w.p, gh, w.list, sc, w.status);
+  paged_schedule<kBN, kMaxRows, kMmaThreads, 0>(w.p, gh, w.list, sc, w.status);
   __syncthreads();
 
   let_next_start();
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kFThreads)
   PagedScan* sc = reinterpret_cast<PagedScan*>(smem_raw + C::kOffScan);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gh = w.by_group.d;
-  paged_schedule<kFBN, kFRows, kFThreads>(w.p, gh, w.list, sc, w.status);
+  paged_schedule<kFBN, kFRows, kFThreads, 0>(w.p, gh, w.list, sc, w.status);
   __syncthreads();
   let_next_start();
   PagedWalk<kFBN, kFRows> k;
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kFThreads)
       }
       __syncthreads();  // the buffer is free for the tile after next
     }
-    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ps);
+    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ts);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float sum = l[e];
@@ -623,19 +623,19 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
   // a row's partials of one item: rows at + j * kStep for j < count
   struct Place {
-    int seg, nt, ts, ps, in_tile, j, n;  // segment, its key tiles, log2 tile and partial rows, row in the tile; item, items
+    int seg, nt, ts, in_tile, j, n;  // segment, its key tiles, log2 rows a tile, row in the tile; item of its list, items
   };
   auto place = [&](auto span, const PagedList& l, int i) -> Place {
     using Span = decltype(span);
     const PagedItem it = paged_item(w.p, i);
     const Span sp(it, gh);
     const int g = w.by_group(h), r = (t - it.t0 - g) * gh + h;
-    return Place{g * sp.rt + (r >> sp.ts), sp.nt, sp.ts, sp.ps, r & ((1 << sp.ts) - 1), i - l.begin, l.end - l.begin};
+    return Place{g * sp.rt + (r >> sp.ts), sp.nt, sp.ts, r & ((1 << sp.ts) - 1), i - l.begin, l.end - l.begin};
   };
   const bool own_list = w.prefix.end > 0;
   const int limit = paged_limit(w.p, b, t);
   constexpr int kPrefixRows = paged_prefix_rows(D);
-  Place pp{0, 0, 0, 0, 0, 0, 0};
+  Place pp{0, 0, 0, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
     pp = own_list ? place(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
@@ -650,20 +650,18 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> long long {
     count = 0;
     if (p.nt == 0) return 0;
-    const long long total = l.items[p.n], u0 = l.items[p.j] + static_cast<long long>(p.seg) * p.nt;
-    const long long row = l.items[p.n + 1 + p.j];
-    const int c0 = paged_owner(u0, total, l.ctas), c1 = paged_owner(u0 + p.nt - 1, total, l.ctas);
+    const PagedCut cut{l.items[p.n], static_cast<int>(l.items[p.n + 1]), l.ctas};
+    const long long u0 = l.items[p.j] + static_cast<long long>(p.seg) * cut.padded(p.nt);
+    const long long row = l.items[p.n + 2 + p.j];
+    const int c0 = cut.owner(u0), c1 = cut.owner(u0 + p.nt - 1);
     count = c1 - c0 + 1;
-    return paged_part_row(c0, step, row, p.seg, p.ps) + p.in_tile;
+    return paged_part_row(c0, step, row, p.seg, p.ts) + p.in_tile;
   };
   const PagedList& pl = own_list ? w.prefix : w.list;
   const int pstep = own_list ? kPrefixRows : kMax;
   int pcount, ocount;
   const long long pfirst = first_row(pp, pl, pstep, pcount);
   const long long ofirst = first_row(po, w.list, kMax, ocount);
-  // a prefix's partials: one a CTA, or two (a tile apart) where its lanes took turns
-  const int halves = pp.ps - pp.ts;
-  pcount <<= halves;
   const int all = pcount + ocount;
   float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
@@ -680,7 +678,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
       if (j < all) {
         const bool pre = j < pcount;
-        const long long r = pre ? pfirst + static_cast<long long>(j >> halves) * pstep + ((halves & j) << pp.ts)
+        const long long r = pre ? pfirst + static_cast<long long>(j) * pstep
                                 : ofirst + static_cast<long long>(j - pcount) * kMax;
         ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
         const float* o = (pre ? pl.part_o : w.list.part_o) + r * D;
@@ -692,10 +690,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       top = fmaxf(top, ml[i].x);
-      if (ml[i].y == 0.f) {  // no weight: O may be unwritten, or 0 * NaN
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
-      }
     }
     const float base = top == -INFINITY ? 0.f : top;
     const float f = ex2_approx(m - base);
@@ -830,11 +824,10 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
   PagedShape s{};
   const int gh = num_q_heads / p.num_kv_heads;
   const bool bf16 = dtype == DHSA_BF16;
-  // rows padded to tiles of 2^ts, each tile's partials of 2^ps rows
-  auto padded = [](long long r, int ts, int ps) { return (r + (1 << ts) - 1) >> ts << ps; };
+  auto padded = [](long long r, int ts) { return (r + (1 << ts) - 1) >> ts << ts; };  // to tiles of 2^ts
   auto list_rows = [&](long long r) {
     const int ts = bf16 ? paged_tile_shift<kMaxRows>(static_cast<int>(r)) : paged_tile_shift<kFRows>(static_cast<int>(r));
-    return padded(r, ts, ts);
+    return padded(r, ts);
   };
   const bool wide = paged_prefix_rows(p.head_dim) == 256;
   long long most = 0, prefix = 0, list = 0, groups_in_list = 0;
@@ -842,7 +835,7 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
     const long long r = static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
     most = r > most ? r : most;
     const int ts = wide ? paged_tile_shift<256>(static_cast<int>(r)) : paged_tile_shift<128>(static_cast<int>(r));
-    prefix += padded(r, ts, wide ? paged_part_shift<256>(ts) : ts);
+    prefix += padded(r, ts);
     groups_in_list += list_rows(r);
   }
   for (int b = 0; b < p.num_seqs; ++b) list += list_rows(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);

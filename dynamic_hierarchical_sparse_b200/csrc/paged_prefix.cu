@@ -14,7 +14,7 @@
 // tensor core works for one while the other's softmax runs.  A row tile of more
 // than 128 rows gives each lane half of them and every key tile feeds both; with
 // 128 rows or fewer, where the call is bound by reading keys, both lanes have
-// the same rows and take every other key tile (two partials a piece).  K and V
+// the same rows and take every other key tile, and join when the piece ends.  K and V
 // tiles come into rings of 2 and 3 (4 and 4 for d 64).  P is handed over in two
 // halves of 64 keys, so the first half's products run beside the second half's
 // exponentials.  d 256 has TMEM and shared memory for one lane.
@@ -39,6 +39,26 @@ constexpr int kBN = kPrefixBN;
 // relative rounding (2^-11), and most tiles skip the pass over O.
 constexpr float kRescaleLog2 = 8.0f;
 
+// A lane's two 32-bit columns, stored and loaded.
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t x, uint32_t y) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t& x, uint32_t& y) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x), "=r"(y)
+      : "r"(taddr)
+      : "memory");
+}
+
+// Eight fp32 numbers of a row, a whole 32-byte sector, in one store.
+__device__ __forceinline__ void store_row8(float* dst, const uint32_t* o) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+               "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
+
 // 32 lanes x 16 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -48,6 +68,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+
+enum {
+  kBarKFull = 0,    // + stage
+  kBarVFull = 4,    // + stage
+  kBarKFree = 8,    // + stage: S of the tile done (one commit a lane, or two of one lane)
+  kBarVFree = 12,   // + stage: P V of the tile done
+  kBarSFull = 16,   // + lane
+  kBarPHalf = 18,   // + lane: first 64 keys of P written, O rescaled
+  kBarPFull = 20,   // + lane
+  kBarQFull = 22,   // + lane: a piece's Q in shared memory
+  kBarODone = 24,   // + lane: a piece's last P V done
+  kBarDrain = 26,   // + lane
+  kBarTurn = 28,    // + lane: that lane's thread ended a turn
+  kBarCross = 30,   // + lane: its (m, l) is in TMEM and its O complete
+  kBarPiece = 32,   // both lanes have read a piece's results
+  kNumBars = 33
+};
+
+// A second piece costs a CTA about as much as this many key tiles (8 us of
+// epilogue, Q and first tiles against 1.5 to 2 us a tile).
+constexpr int kSnapTiles = 4;
 
 template <int D>
 struct PrefixCfg {
@@ -67,27 +108,12 @@ struct PrefixCfg {
   static constexpr int kOffV = kOffK + kKStages * kTile;
   static constexpr int kOffScan = kOffV + kVStages * kTile;
   static constexpr int kOffBar = kOffScan + ((static_cast<int>(sizeof(PagedScan)) + 15) / 16) * 16;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;              // + 128 * lane
   static constexpr uint32_t kColO = 128 * kLanes;   // + D * lane
   static_assert(kLanes * (128 + D) <= 512, "TMEM budget");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-};
-
-enum {
-  kBarKFull = 0,    // + stage
-  kBarVFull = 4,    // + stage
-  kBarKFree = 8,    // + stage: S of the tile done (one commit a lane, or two of one lane)
-  kBarVFree = 12,   // + stage: P V of the tile done
-  kBarSFull = 16,   // + lane
-  kBarPHalf = 18,   // + lane: first 64 keys of P written, O rescaled
-  kBarPFull = 20,   // + lane
-  kBarQFull = 22,   // + lane: a piece's Q in shared memory
-  kBarODone = 24,   // + lane: a piece's last P V done
-  kBarDrain = 26,   // + lane
-  kBarTurn = 28,    // + lane: that lane's thread ended a turn
-  kNumBars = 30
 };
 
 template <int D>
@@ -122,7 +148,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       mbar_init(bar(kBarODone + a), 1);
       mbar_init(bar(kBarDrain + a), 1);
       mbar_init(bar(kBarTurn + a), 1);
+      mbar_init(bar(kBarCross + a), 4);
     }
+    mbar_init(bar(kBarPiece), 4 * C::kLanes);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -143,7 +171,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     // 8 warps x 224 + 4 x 56 registers = the launch's 12 x 168
     if constexpr (C::kLanes == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // this warpgroup lays out the CTA's work while the softmax warps warm up
-    paged_schedule<kBN, C::kRows, 128>(w.p, gh, w.prefix, sc, w.status);
+    paged_schedule<kBN, C::kRows, 128, kSnapTiles>(w.p, gh, w.prefix, sc, w.status);
     let_next_start();
     __syncthreads();
     const bool work = walk.init(&w.p, gh, w.prefix, sc);
@@ -289,7 +317,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + C::kColS + 128 * a, tO = tmem + lane_base + C::kColO + D * a;
     const float scale_log2 = w.scale * kLog2e;
-    int n0 = 0, mine = 0, ends = 0;  // key tiles, this lane's tiles and its pieces with any: across pieces
+    // key tiles and this lane's tiles; pieces, those in which lane 1 has a tile, those with lanes apart: so far
+    int n0 = 0, mine = 0, done[2] = {0, 0}, joins = 0;
     bool ok = true;
     // The first round is a rehearsal: the code below comes a cache line at a
     // time from L2 the first time that it runs (6 us for a tile's softmax,
@@ -493,21 +522,19 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         send_q(walk);
         continue;
       }
-      const long long part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ps) + in_tile +
-                             (ap ? a << walk.ts : 0);  // lanes apart: lane 1's rows lie behind lane 0's
+      const long long part =
+          paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ts) + in_tile;
+      float* dst = w.prefix.part_o + part * D;
+      const bool some = kt0 < count;  // lanes apart: lane 1 has no tile in a piece of one
       const bool more = walk.next();
       if (more) send_q(walk);
-      const bool any_tile = kt0 < count;
-      if (any_tile) {
-        if (!(ok = mbar_wait(bar(kBarODone + a), ends & 1, abort_flag, w.status))) break;
-        ++ends;
+      if (some) {
+        if (!(ok = mbar_wait(bar(kBarODone + a), done[a] & 1, abort_flag, w.status))) break;
         tc_fence_after();
       }
-      if (warp_valid) {
-        // a lane without a tile says so by its sum of 0
-        if (valid) w.prefix.part_ml[part] = make_float2(m_run, l_run);
-        float* dst = w.prefix.part_o + part * D;
-        if (any_tile) {
+      if (!ap) {
+        if (warp_valid) {
+          if (valid) w.prefix.part_ml[part] = make_float2(m_run, l_run);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -516,15 +543,68 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             reg_dep32(o);
             if (valid) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 8) store_row8(dst + 32 * c + e, o + e);
             }
           }
           tc_fence_before();  // the next piece's P V overwrites O after this warp's next arrival
         }
+      } else {
+        // Lanes apart: their results of a row join here, each lane finishing
+        // half of the columns.  A thread of either lane sees the row's both O in
+        // TMEM; (m, l) cross over there, too, in columns that P has left.
+        tmem_st2(tS, __float_as_uint(m_run), __float_as_uint(l_run));
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarCross + a));
+        if (!(ok = mbar_wait(bar(kBarCross + 1 - a), joins & 1, abort_flag, w.status))) break;
+        tc_fence_after();
+        if (warp_valid) {
+          uint32_t xm, xl;
+          tmem_ld2(tmem + lane_base + C::kColS + 128 * (1 - a), xm, xl);
+          const float om = __uint_as_float(xm), ol = __uint_as_float(xl);
+          const float top = fmaxf(m_run, om);
+          const float base = top == -INFINITY ? 0.f : top;
+          const float f = ex2_approx(m_run - base), g = ex2_approx(om - base);
+          const float f0 = a == 0 ? f : g, f1 = a == 0 ? g : f;  // of lane 0's and lane 1's O
+          const bool both = count > 1;
+          if (valid && a == 0) w.prefix.part_ml[part] = make_float2(top, fmaf(l_run, f, ol * g));
+          constexpr int kHalf = D / 2;
+#pragma unroll 1
+          for (int c = 0; c < kHalf / 32; ++c) {
+            uint32_t o0[32], o1[32];
+            const uint32_t at = tmem + lane_base + C::kColO + a * kHalf + 32 * c;
+            tmem_ld32(at, o0);
+            tmem_ld32(at + D, o1);
+            tmem_wait_ld();
+            reg_dep32(o0);
+            reg_dep32(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o0[e] = __float_as_uint(
+                  fmaf(__uint_as_float(o0[e]), f0, both ? __uint_as_float(o1[e]) * f1 : 0.f));
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) store_row8(dst + a * kHalf + 32 * c + e, o0 + e);
+            }
+          }
+          tc_fence_before();
+        }
+        ++joins;
       }
+      if constexpr (C::kLanes == 2) {
+        if (!more) break;
+        // no product of the next piece starts before both lanes have read TMEM
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPiece));
+        if (!(ok = mbar_wait(bar(kBarPiece), (done[0]) & 1, abort_flag, w.status))) break;
+      } else {
+        if (!more) break;
+      }
+      // lane 0 has a tile in every piece
+      ++done[0];
+      if (!ap || count > 1) ++done[1];
       n0 += count;
-      if (!more) break;
     } while (true);
   }
 

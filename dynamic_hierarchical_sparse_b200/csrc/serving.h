@@ -76,7 +76,7 @@ struct PagedList {
   int ctas;          // CTAs of its grid
   float* part_o;     // [rows of all its partials, d]
   float2* part_ml;   // [rows of all its partials]: running max (log2 units), sum
-  long long* items;  // [2 (end - begin) + 1]: first key tile of each item, the total, then first row of each item
+  long long* items;  // [2 (end - begin) + 2]: first key tile of each item, the total, the chunk, first row of each item
 };
 
 struct PagedWork {

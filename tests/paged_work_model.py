@@ -10,8 +10,8 @@ def tile_rows(rows, most):
 
 
 def part_tile(tm, most):
-    """Rows of a segment's partials: two partials of small tiles where tiles reach 256 rows."""
-    return 2 * tm if most == 256 and tm <= 128 else tm
+    """Rows of a segment's partials."""
+    return tm
 
 
 def spans(items, hkv, bn, most):
@@ -26,26 +26,53 @@ def spans(items, hkv, bn, most):
     return out
 
 
-def pieces(items, hkv, bn, most, ctas):
+def cut(items, hkv, bn, most, ctas, snap):
+    """(total units, chunk): as paged_schedule decides them; units padded to whole chunks where chunk > 0."""
+    sp = spans(items, hkv, bn, most)
+    total, segs = sum(x[0] for x in sp), sum(hkv * x[3] for x in sp if x[4] > 0)
+    chunk = 0
+    if snap > 0 and 2 * segs < ctas and total > 0:
+        want = -(-total // (ctas - segs))
+        if want <= total // ctas + snap:
+            chunk = want
+    return sum(hkv * x[3] * padded(x[4], chunk) for x in sp), chunk
+
+
+def padded(nt, chunk):
+    return -(-nt // chunk) * chunk if chunk else nt
+
+
+def first(c, total, chunk, ctas):
+    if chunk:
+        return min(c * chunk, total)
+    n = min(ctas, total)
+    return c * total // n if c < n else total
+
+
+def owner(unit, total, chunk, ctas):
+    return unit // chunk if chunk else ((unit + 1) * min(ctas, total) - 1) // total
+
+
+def pieces(items, hkv, bn, most, ctas, snap=0):
     """Every piece of every CTA: (cta, item, segment, first key tile, tiles, first partial row, rows)."""
     sp = spans(items, hkv, bn, most)
-    total = sum(s[0] for s in sp)
-    ctas = min(ctas, total)
+    total, chunk = cut(items, hkv, bn, most, ctas, snap)
     got = []
     for c in range(ctas):
-        u0, u1 = c * total // ctas, (c + 1) * total // ctas
-        left = u1 - u0
+        u0 = first(c, total, chunk, ctas)
+        left = first(c + 1, total, chunk, ctas) - u0
         if left <= 0:
             continue
         unit = row = i = 0
-        while not (sp[i][0] > 0 and unit <= u0 < unit + sp[i][0]):
-            unit, row, i = unit + sp[i][0], row + sp[i][1], i + 1
-        seg, kt = divmod(u0 - unit, sp[i][4])
+        units = lambda x: hkv * sp[x][3] * padded(sp[x][4], chunk)  # noqa: E731
+        while not (units(i) > 0 and unit <= u0 < unit + units(i)):
+            unit, row, i = unit + units(i), row + sp[i][1], i + 1
+        seg, kt = divmod(u0 - unit, padded(sp[i][4], chunk))
         count = min(sp[i][4] - kt, left)
         while True:
             got.append((c, i, seg, kt, count, c * most + row + seg * sp[i][2], sp[i][2]))
             left -= count
-            if left <= 0:
+            if chunk or left <= 0:
                 break
             kt, seg = 0, seg + 1
             if seg == hkv * sp[i][3]:
@@ -54,9 +81,4 @@ def pieces(items, hkv, bn, most, ctas):
                 while sp[i][4] == 0:
                     row, i = row + sp[i][1], i + 1
             count = min(sp[i][4], left)
-    return got, sp, total
-
-
-def owner(unit, total, ctas):
-    ctas = min(ctas, total)
-    return ((unit + 1) * ctas - 1) // total
+    return got, sp, total, chunk
