@@ -132,12 +132,13 @@ dhsa_status attention_layout(const dhsa_paged_cache* c, const dhsa_paged_batch* 
   if (num_q_heads > 65535) return DHSA_ERR_UNSUPPORTED;
   if (static_cast<long long>(a.total_q) * num_q_heads > INT32_MAX) return DHSA_ERR_UNSUPPORTED;
   L->shape = paged_shape(a, b->h_cu_q, b->h_group_ptr, num_q_heads, c->dtype);
+  if (!L->shape.fits) return DHSA_ERR_UNSUPPORTED;
   size_t at = kStatusBytes;
   for (int x = 0; x < 2; ++x) {
     const size_t rows = static_cast<size_t>(x == 0 ? L->shape.prefix_rows : L->shape.list_rows);
     const size_t n = static_cast<size_t>(x == 0 ? L->shape.prefix_items : L->shape.list_items);
     L->items[x] = at;
-    at += align_up((2 * n + 2) * sizeof(long long));
+    at += align_up((2 * n + 2) * sizeof(int));
     L->ml[x] = at;
     at += align_up(rows * sizeof(float2));
     L->o[x] = at;
@@ -331,11 +332,11 @@ dhsa_status dhsa_paged_attention(const dhsa_paged_cache* cache, const dhsa_paged
   w.list.end = groups + w.p.num_seqs;
   for (int x = 0; x < 2; ++x) {
     PagedList& l = x == 0 ? w.prefix : w.list;
-    l.items = reinterpret_cast<long long*>(ws + L.items[x]);
+    l.items = reinterpret_cast<int*>(ws + L.items[x]);
     l.part_ml = reinterpret_cast<float2*>(ws + L.ml[x]);
     l.part_o = reinterpret_cast<float*>(ws + L.o[x]);
   }
-  return cuda_status(launch_paged_attention(w, cache->dtype, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_paged_attention(w, L.shape, cache->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -116,47 +116,46 @@ struct PagedSpan {
   }
 };
 
-// (Products within 32 bits, the usual case, divide several times faster.)
-__device__ __forceinline__ long long paged_divide(long long a, long long b) {
-  if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// How a list's key tiles (units) are cut among the CTAs.  chunk 0: evenly,
-// wherever that falls; with fewer units than CTAs the first `total` CTAs take
-// one each, so every CTA between the first and the last owner of a segment has
-// a partial of it.  chunk > 0: every segment counts as a whole number of chunks,
-// a CTA takes one chunk, and none has two segments.
+// How a list's key tiles (units, fewer than 2^30) are cut among the CTAs.
+// chunk 0: evenly, wherever that falls; with fewer units than CTAs the first
+// `total` CTAs take one each, so every CTA between the first and the last owner
+// of a segment has a partial of it.  chunk > 0: every segment counts as a whole
+// number of chunks, a CTA takes one chunk, and none has two segments.
 struct PagedCut {
-  long long total;
-  int chunk, ctas;
-  __device__ __forceinline__ int used() const { return static_cast<int>(min(total, static_cast<long long>(ctas))); }
+  int total, chunk;
+  FastDiv by_ctas;
   __device__ __forceinline__ int padded(int nt) const {
     return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt;
   }
-  __device__ __forceinline__ long long first(long long c) const {  // the first unit of CTA c
+  __device__ __forceinline__ int first(int c) const {  // the first unit of CTA c: c * total / ctas
     if (chunk > 0) return min(c * chunk, total);
-    const int n = used();
-    return c < n ? paged_divide(c * total, n) : total;
+    const int n = by_ctas.d;
+    if (total <= n) return min(c, total);
+    const int q = by_ctas(total);
+    return c * q + by_ctas(c * (total - q * n));
   }
-  __device__ __forceinline__ int owner(long long unit) const {  // the CTA that holds a unit
-    return static_cast<int>(chunk > 0 ? paged_divide(unit, chunk) : paged_divide((unit + 1) * used() - 1, total));
+  __device__ __forceinline__ int owner(int unit) const {  // the CTA that holds a unit
+    if (chunk > 0) return unit / chunk;
+    const int n = by_ctas.d;
+    if (total <= n) return unit;
+    // ((unit + 1) * ctas - 1) / total; 32 bits divide several times faster than 64
+    const unsigned long long x = static_cast<unsigned long long>(unit + 1) * n - 1;
+    return static_cast<int>(x >> 32 == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(total) : x / total);
   }
 };
 
 // Where CTA c's partial of a segment starts (rows): c steps by the largest
 // tile, a segment by its own rows, and along the list either c or the segment moves
 // on, so no two partials overlap.
-__device__ __forceinline__ long long paged_part_row(int c, int max_rows, long long item_row, int seg, int ts) {
-  return static_cast<long long>(c) * max_rows + item_row + (static_cast<long long>(seg) << ts);
+__device__ __forceinline__ int paged_part_row(int c, int max_rows, int item_row, int seg, int ts) {
+  return c * max_rows + item_row + (seg << ts);
 }
 
 // Shared-memory words of the block-wide scan.
 struct PagedScan {
-  long long warp_units[8], warp_rows[8];
-  int warp_segs[8];
+  int warp_units[8], warp_rows[8], warp_segs[8];
   PagedCut cut;
-  long long item_unit, item_row;
+  int item_unit, item_row;
   PagedItem it;
   int item;
 };
@@ -177,15 +176,15 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
   const int i0 = min(thread * per, n), i1 = min(i0 + per, n);
   const int lane = thread & 31, warp = thread >> 5;
   auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-  PagedCut cut{0, 0, static_cast<int>(gridDim.x)};
-  long long base_u = 0, base_r = 0;
+  PagedCut cut{0, 0, list.by_ctas};
+  int base_u = 0, base_r = 0;
   // rounds (one body, so that its code comes in once): the plain count with
   // its segments (kSnap), the padded count, then the finding of this CTA's item
 #pragma unroll 1
   for (int round = kSnap > 0 ? 0 : 1; round < 3; ++round) {
     const bool find = round == 2;
-    const long long mine = find ? cut.first(blockIdx.x) : 0;
-    long long units = base_u, rows = base_r;
+    const int mine = find ? cut.first(blockIdx.x) : 0;
+    int units = base_u, rows = base_r;
     if (!find) units = rows = 0;
     int segs = 0;
     bool bad = false;
@@ -193,8 +192,8 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
       const PagedItem it = paged_item(p, list.begin + i);
       const PagedSpan<BN, kMaxRows> sp(it, group_heads);
       const int tiles = p.num_kv_heads * sp.rt;
-      const long long du = static_cast<long long>(tiles) * cut.padded(sp.nt);
-      const long long dr = static_cast<long long>(tiles) << sp.ts;
+      const int du = tiles * cut.padded(sp.nt);
+      const int dr = tiles << sp.ts;
       if (find) {
         if (du > 0 && units <= mine && mine < units + du) {
           sc->item = list.begin + i;
@@ -220,10 +219,10 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     }
     if (find) break;
     if (bad) report(status, kDevCheck);
-    long long iu = units, ir = rows;
+    int iu = units, ir = rows;
 #pragma unroll 1
     for (int o = 1; o < 32; o *= 2) {
-      const long long u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
+      const int u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
       if (lane >= o) {
         iu += u;
         ir += r;
@@ -242,7 +241,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     segs = 0;
 #pragma unroll 1
     for (int x = 0; x < kThreads / 32; ++x) {
-      const long long u = sc->warp_units[x];
+      const int u = sc->warp_units[x];
       if (x < warp) {
         base_u += u;
         base_r += sc->warp_rows[x];
@@ -251,10 +250,10 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
       segs += sc->warp_segs[x];
     }
     if (kSnap > 0 && round == 0) {
-      if (2 * segs < cut.ctas && cut.total > 0) {
-        const long long spare = cut.ctas - segs;
-        const long long chunk = paged_divide(cut.total + spare - 1, spare);
-        if (chunk <= paged_divide(cut.total, cut.ctas) + kSnap) cut.chunk = static_cast<int>(chunk);
+      const int ctas = list.by_ctas.d;
+      if (2 * segs < ctas && cut.total > 0) {
+        const int chunk = (cut.total + ctas - segs - 1) / (ctas - segs);
+        if (chunk <= list.by_ctas(cut.total) + kSnap) cut.chunk = chunk;
       }
       meet();  // the words above are read before the next round writes them
     }
@@ -267,7 +266,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
           list.items[n + 1] = cut.chunk;
         }
       }
-      const long long first = cut.first(blockIdx.x);
+      const int first = cut.first(blockIdx.x);
       if (blockIdx.x != 0 && !(units > 0 && base_u <= first && first < base_u + units)) break;
     }
   }
@@ -282,7 +281,7 @@ struct PagedWalk {
   int i;
   PagedItem it;
   int ts, rt, first, nt;
-  long long item_row, left;
+  int item_row, left;
   int h, ri;      // current piece: KV head, row tile,
   int kt, count;  // first key tile (of the item), tiles
 
@@ -302,7 +301,7 @@ struct PagedWalk {
     group_heads = gh;
     end = list.end;
     const PagedCut& cut = sc->cut;
-    const long long u0 = cut.first(blockIdx.x);
+    const int u0 = cut.first(blockIdx.x);
     left = cut.first(blockIdx.x + 1) - u0;
     if (left <= 0) return false;
     one = cut.chunk > 0;
@@ -310,13 +309,12 @@ struct PagedWalk {
     it = sc->it;
     item_row = sc->item_row;
     measure();
-    const long long off = u0 - sc->item_unit;
-    const int ntp = cut.padded(nt);
-    const int s = static_cast<int>(paged_divide(off, ntp));
-    kt = static_cast<int>(off - static_cast<long long>(s) * ntp);
+    const int off = u0 - sc->item_unit, ntp = cut.padded(nt);
+    const int s = off / ntp;
+    kt = off - s * ntp;
     h = rt == 1 ? s : s / rt;
     ri = s - h * rt;
-    count = static_cast<int>(min(static_cast<long long>(nt - kt), left));
+    count = min(nt - kt, left);
     return true;
   }
   __device__ __forceinline__ bool next() {
@@ -328,14 +326,14 @@ struct PagedWalk {
       if (++h == p->num_kv_heads) {
         h = 0;
         do {
-          item_row += static_cast<long long>(p->num_kv_heads) * rt << ts;
+          item_row += p->num_kv_heads * rt << ts;
           if (++i >= end) return false;
           it = paged_item(*p, i);
           measure();
         } while (nt == 0);
       }
     }
-    count = static_cast<int>(min(static_cast<long long>(nt), left));
+    count = min(nt, left);
     return true;
   }
 };

@@ -28,13 +28,19 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Groups of more rows (query tokens times Hq / Hkv) than this have their
-// prefixes worked on by the tcgen05 kernel.
+// The prefixes are a list of their own, for the tcgen05 kernel, where a group
+// has more than 32 rows (query tokens times Hq / Hkv) and the prefixes may be
+// long: rows x Hkv x d x the tokens that a table row has room for (their lengths
+// are on the device) of 2^30 or more.  That kernel costs about 10 us more to
+// start and end; 32 + 8 heads of 128, page 16, one kernel / two, in us: 16
+// sequences on 1024 keys 21.9 / 27.9, on 8192 30.9 / 36.7, 32 on 2048 28.4 /
+// 37.5, 12 on 32768 58.0 / 53.7, 32 on 32768 106 / 71; 64 of d 64 on 1024
+// 27.0 / 35.7; 24 sequences of 5 tokens, 8 + 4 heads of 256, on 4097 62 / 50.
 constexpr int kOwnPrefixRows = 32;
+constexpr long long kOwnPrefixWork = 1ll << 30;
 
 // ------------------------------------------------------------------ bf16
 constexpr int kBN = 64;        // keys a tile
-constexpr int kMaxRows = 64;   // rows a tile at most
 constexpr int kMmaThreads = 160;  // four compute warps, one producer
 constexpr int kProducer = 4;
 
@@ -113,8 +119,8 @@ __device__ __forceinline__ bool compute_sync_or(bool x) {
 
 // One piece on the four compute warps: WM warps along the rows, WN along a
 // tile's keys.  false: a warp's wait gave up.
-template <int D, int WM, int WN>
-__device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kBN, kMaxRows>& k, MmaCtx& ctx) {
+template <int D, int kMax, int WM, int WN>
+__device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kBN, kMax>& k, MmaCtx& ctx) {
   using C = MmaCfg<D>;
   constexpr int kWarpKeys = kBN / WN;
   constexpr int kSub = WN == 4 ? 16 : (D == 256 ? 16 : 32);  // keys of one softmax step
@@ -303,7 +309,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
     f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
   }
-  const long long part = paged_part_row(blockIdx.x, kMaxRows, k.item_row, k.seg(), k.ts);
+  const int part = paged_part_row(blockIdx.x, kMax, k.item_row, k.seg(), k.ts);
   const int valid = min(rows - row0, WM * 16);
   if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
     const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
@@ -340,14 +346,16 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
         a.z += u.z;
         a.w += u.w;
       }
-      *reinterpret_cast<float4*>(w.list.part_o + (part + r) * D + c * (D / 4) + 4 * v) = a;
+      *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + c * (D / 4) + 4 * v) = a;
     }
     if (c < 3) compute_sync();
   }
   return !compute_sync_or(!ok);
 }
 
-template <int D>
+// kMax: rows a tile at most, 64, or 16 for a list without more (decode steps
+// mostly), whose kernel then is a third of the code.
+template <int D, int kMax>
 __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ PagedWork w) {
@@ -377,11 +385,11 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  paged_schedule<kBN, kMaxRows, kMmaThreads, 0>(w.p, gh, w.list, sc, w.status);
+  paged_schedule<kBN, kMax, kMmaThreads, 0>(w.p, gh, w.list, sc, w.status);
   __syncthreads();
 
   let_next_start();
-  PagedWalk<kBN, kMaxRows> walk;
+  PagedWalk<kBN, kMax> walk;
   if (!walk.init(&w.p, gh, w.list, sc)) {  // uniform for the CTA
     wait_for_previous();
     return;
@@ -440,12 +448,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
   } else {
     bool ok;
     do {
-      if (walk.ts == 4) {
-        ok = mma_piece<D, 1, 4>(w, walk, ctx);
-      } else if (walk.ts == 5) {
-        ok = mma_piece<D, 2, 2>(w, walk, ctx);
-      } else {
-        ok = mma_piece<D, 4, 1>(w, walk, ctx);
+      if (kMax == 16 || walk.ts == 4) {
+        ok = mma_piece<D, kMax, 1, 4>(w, walk, ctx);
+      } else if constexpr (kMax > 16) {
+        ok = walk.ts == 5 ? mma_piece<D, kMax, 2, 2>(w, walk, ctx) : mma_piece<D, kMax, 4, 1>(w, walk, ctx);
       }
     } while (ok && walk.next());
   }
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(kFThreads)
       }
       __syncthreads();  // the buffer is free for the tile after next
     }
-    const long long part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ts);
+    const int part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ts);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float sum = l[e];
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kFThreads)
       if (row0 + r < rows) {
         if (lane == 0) w.list.part_ml[part + r] = make_float2(m[e], sum);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) w.list.part_o[(part + r) * D + c * 32 + lane] = o[e][c];
+        for (int c = 0; c < kCols; ++c) w.list.part_o[static_cast<long long>(part + r) * D + c * 32 + lane] = o[e][c];
       }
     }
   } while (k.next());
@@ -647,12 +653,12 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     if (w.lse != nullptr && threadIdx.x == 0) w.lse[static_cast<long long>(t) * w.num_q_heads + h] = -INFINITY;
     return;
   }
-  auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> long long {
+  auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> int {
     count = 0;
     if (p.nt == 0) return 0;
-    const PagedCut cut{l.items[p.n], static_cast<int>(l.items[p.n + 1]), l.ctas};
-    const long long u0 = l.items[p.j] + static_cast<long long>(p.seg) * cut.padded(p.nt);
-    const long long row = l.items[p.n + 2 + p.j];
+    const PagedCut cut{l.items[p.n], l.items[p.n + 1], l.by_ctas};
+    const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt);
+    const int row = l.items[p.n + 2 + p.j];
     const int c0 = cut.owner(u0), c1 = cut.owner(u0 + p.nt - 1);
     count = c1 - c0 + 1;
     return paged_part_row(c0, step, row, p.seg, p.ts) + p.in_tile;
@@ -660,8 +666,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const PagedList& pl = own_list ? w.prefix : w.list;
   const int pstep = own_list ? kPrefixRows : kMax;
   int pcount, ocount;
-  const long long pfirst = first_row(pp, pl, pstep, pcount);
-  const long long ofirst = first_row(po, w.list, kMax, ocount);
+  const int pfirst = first_row(pp, pl, pstep, pcount);
+  const int ofirst = first_row(po, w.list, kMax, ocount);
   const int all = pcount + ocount;
   float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
@@ -678,10 +684,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
       if (j < all) {
         const bool pre = j < pcount;
-        const long long r = pre ? pfirst + static_cast<long long>(j) * pstep
-                                : ofirst + static_cast<long long>(j - pcount) * kMax;
+        const int r = pre ? pfirst + j * pstep : ofirst + (j - pcount) * kMax;
         ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
-        const float* o = (pre ? pl.part_o : w.list.part_o) + r * D;
+        const float* o = (pre ? pl.part_o : w.list.part_o) + static_cast<long long>(r) * D;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) x[i][c] = o[c * 32 + lane];
       }
@@ -765,25 +770,25 @@ cudaError_t join(const PagedWork& w, cudaStream_t stream) {
   return launch_after(paged_join_kernel<D, T, BN, kMax>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, true, w);
 }
 
-template <int D>
+template <int D, int kMax>
 cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   using C = MmaCfg<D>;
   CUtensorMap mk, mv;
   if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, false) != CUDA_SUCCESS ||
       encode_pages_map(&mv, w.p.v_pages, w.p, kBN, true) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, kMax>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  w.list.ctas = sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas;
+  w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
   if (w.prefix.end > 0) {
-    w.prefix.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    w.prefix.by_ctas = FastDiv(sms < kMaxCtas ? sms : kMaxCtas);
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
   }
-  e = launch_after(paged_mma_kernel<D>, w.list.ctas, kMmaThreads, C::kSmemBytes, stream, w.prefix.end > 0, mk, mv, w);
+  e = launch_after(paged_mma_kernel<D, kMax>, w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream, w.prefix.end > 0, mk, mv, w);
   if (e != cudaSuccess) return e;
-  return join<D, __nv_bfloat16, kBN, kMaxRows>(w, stream);
+  return join<D, __nv_bfloat16, kBN, kMax>(w, stream);
 }
 
 template <int D>
@@ -794,8 +799,8 @@ cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   const int per_sm = D == 256 ? 1 : D == 128 ? 2 : 3;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  w.list.ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
-  paged_f32_kernel<D><<<w.list.ctas, kFThreads, C::kSmemBytes, stream>>>(w);
+  w.list.by_ctas = FastDiv(sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas);
+  paged_f32_kernel<D><<<w.list.by_ctas.d, kFThreads, C::kSmemBytes, stream>>>(w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return join<D, float, kFBN, kFRows>(w, stream);
@@ -822,39 +827,54 @@ CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p
 
 PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group_ptr, int num_q_heads, int dtype) {
   PagedShape s{};
-  const int gh = num_q_heads / p.num_kv_heads;
-  const bool bf16 = dtype == DHSA_BF16;
-  auto padded = [](long long r, int ts) { return (r + (1 << ts) - 1) >> ts << ts; };  // to tiles of 2^ts
-  auto list_rows = [&](long long r) {
-    const int ts = bf16 ? paged_tile_shift<kMaxRows>(static_cast<int>(r)) : paged_tile_shift<kFRows>(static_cast<int>(r));
-    return padded(r, ts);
+  const int gh = num_q_heads / p.num_kv_heads, G = p.num_groups, cap = p.max_pages * p.page_size;
+  const bool bf16 = dtype == DHSA_BF16, wide = paged_prefix_rows(p.head_dim) == 256;
+  auto group_rows = [&](int g) -> long long {
+    return static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
   };
-  const bool wide = paged_prefix_rows(p.head_dim) == 256;
-  long long most = 0, prefix = 0, list = 0, groups_in_list = 0;
-  for (int g = 0; g < p.num_groups; ++g) {
-    const long long r = static_cast<long long>(h_cu_q[h_group_ptr[g + 1]] - h_cu_q[h_group_ptr[g]]) * gh;
-    most = r > most ? r : most;
-    const int ts = wide ? paged_tile_shift<256>(static_cast<int>(r)) : paged_tile_shift<128>(static_cast<int>(r));
-    prefix += padded(r, ts);
-    groups_in_list += list_rows(r);
+  auto seq_rows = [&](int b) -> long long { return static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh; };
+  long long most_g = 0, all_g = 0, most_s = 0;
+  for (int g = 0; g < G; ++g) {
+    const long long r = group_rows(g);
+    most_g = r > most_g ? r : most_g;
+    all_g += r;
   }
-  for (int b = 0; b < p.num_seqs; ++b) list += list_rows(static_cast<long long>(h_cu_q[b + 1] - h_cu_q[b]) * gh);
-  s.own_prefix = bf16 && most > kOwnPrefixRows;
-  s.prefix_items = s.own_prefix ? p.num_groups : 0;
-  s.list_items = p.num_groups + p.num_seqs - s.prefix_items;
-  s.prefix_rows = s.own_prefix ? prefix * p.num_kv_heads + static_cast<long long>(kMaxCtas) * paged_prefix_rows(p.head_dim) : 0;
-  s.list_rows = (list + (s.own_prefix ? 0 : groups_in_list)) * p.num_kv_heads +
-                static_cast<long long>(kMaxCtas) * (bf16 ? kMaxRows : kFRows);
+  for (int b = 0; b < p.num_seqs; ++b) most_s = seq_rows(b) > most_s ? seq_rows(b) : most_s;
+  const double work = static_cast<double>(all_g) * p.num_kv_heads * p.head_dim * cap;
+  s.own_prefix = bf16 && most_g > kOwnPrefixRows && work >= static_cast<double>(kOwnPrefixWork);
+  s.prefix_items = s.own_prefix ? G : 0;
+  s.list_items = G + p.num_seqs - s.prefix_items;
+  const long long most = s.own_prefix || most_s > most_g ? most_s : most_g;
+  s.list_max = !bf16 || most <= 16 ? 16 : 64;
+  // row tiles of an item, by the list's largest tile
+  long long units[2] = {0, 0};
+  auto add = [&](long long r, int max, int x, long long& rows) {
+    const int ts = max == 256   ? paged_tile_shift<256>(static_cast<int>(r))
+                   : max == 128 ? paged_tile_shift<128>(static_cast<int>(r))
+                   : max == 64  ? paged_tile_shift<64>(static_cast<int>(r))
+                                : paged_tile_shift<16>(static_cast<int>(r));
+    const long long tiles = (r + (1 << ts) - 1) >> ts;
+    rows += tiles * p.num_kv_heads << ts;
+    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 1);
+  };
+  for (int g = 0; g < G; ++g)
+    s.own_prefix ? add(group_rows(g), wide ? 256 : 128, 0, s.prefix_rows)
+                 : add(group_rows(g), s.list_max, 1, s.list_rows);
+  for (int b = 0; b < p.num_seqs; ++b) add(seq_rows(b), s.list_max, 1, s.list_rows);
+  if (s.own_prefix) s.prefix_rows += static_cast<long long>(kMaxCtas) * paged_prefix_rows(p.head_dim);
+  s.list_rows += static_cast<long long>(kMaxCtas) * s.list_max;
+  s.fits = units[0] < (1ll << 30) && units[1] < (1ll << 30) && s.prefix_rows < INT32_MAX && s.list_rows < INT32_MAX;
   return s;
 }
 
-cudaError_t launch_paged_attention(const PagedWork& w, int dtype, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream) {
   if (w.p.total_q <= 0) return cudaSuccess;
   if (dtype == DHSA_BF16) {
+    const bool small = shape.list_max == 16;
     switch (w.p.head_dim) {
-      case 64: return run_mma<64>(w, stream);
-      case 128: return run_mma<128>(w, stream);
-      default: return run_mma<256>(w, stream);
+      case 64: return small ? run_mma<64, 16>(w, stream) : run_mma<64, 64>(w, stream);
+      case 128: return small ? run_mma<128, 16>(w, stream) : run_mma<128, 64>(w, stream);
+      default: return small ? run_mma<256, 16>(w, stream) : run_mma<256, 64>(w, stream);
     }
   }
   switch (w.p.head_dim) {

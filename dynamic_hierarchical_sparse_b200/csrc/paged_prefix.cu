@@ -522,9 +522,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         send_q(walk);
         continue;
       }
-      const long long part =
-          paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ts) + in_tile;
-      float* dst = w.prefix.part_o + part * D;
+      const int part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ts) + in_tile;
+      float* dst = w.prefix.part_o + static_cast<long long>(part) * D;
       const bool some = kt0 < count;  // lanes apart: lane 1 has no tile in a piece of one
       const bool more = walk.next();
       if (more) send_q(walk);
@@ -624,7 +623,7 @@ cudaError_t run(const PagedWork& w, cudaStream_t stream) {
   cudaError_t e =
       cudaFuncSetAttribute(paged_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  paged_prefix_kernel<D><<<w.prefix.ctas, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, w);
+  paged_prefix_kernel<D><<<w.prefix.by_ctas.d, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, w);
   return cudaGetLastError();
 }
 

@@ -73,10 +73,10 @@ cudaError_t launch_kv_append(const PagedArgs& a, int dtype, const dhsa_rope_tabl
 // and the sequences in a list each.
 struct PagedList {
   int begin, end;    // items of the list
-  int ctas;          // CTAs of its grid
+  FastDiv by_ctas;   // by the CTAs of its grid
   float* part_o;     // [rows of all its partials, d]
   float2* part_ml;   // [rows of all its partials]: running max (log2 units), sum
-  long long* items;  // [2 (end - begin) + 2]: first key tile of each item, the total, the chunk, first row of each item
+  int* items;        // [2 (end - begin) + 2]: first key tile of each item, the total, the chunk, first row of each item
 };
 
 struct PagedWork {
@@ -99,11 +99,13 @@ struct PagedWork {
 struct PagedShape {
   bool own_prefix;  // the prefixes are a list of their own
   int prefix_items, list_items;
+  int list_max;  // rows a tile of the list at most
   long long prefix_rows, list_rows;
+  bool fits;     // units and rows within the kernels' 32-bit counts
 };
 PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group_ptr, int num_q_heads, int dtype);
 
-cudaError_t launch_paged_attention(const PagedWork& w, int dtype, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream);
 
 // TMA view of a 16-bit page array; one box is 64 columns of up to `tile` tokens of a page.
 CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16);

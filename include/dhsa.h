@@ -507,7 +507,9 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * below a sequence's kv_lens, or in a shared prefix, may reach all the query
  * rows that are worked on together, also those to which the position is not
  * visible; keys (K), and slots at or behind kv_lens, reach no row that does not
- * see them.  Results are the same from call to call.
+ * see them.  Results are the same from call to call.  A batch whose tables
+ * leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
+ * 32 keys is refused as DHSA_ERR_UNSUPPORTED.
  *   q, out     [T, Hq, d] in the cache's dtype; must not overlap
  *   lse        device fp32 [T, Hq] contiguous, or NULL
  *   workspace  dhsa_paged_attention_workspace_size bytes, 256-byte aligned; a

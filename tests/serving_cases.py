@@ -43,9 +43,11 @@ class Step:
 
     groups: None, or (group_ptr, prefix_lens); the whole pages of a prefix are
     shared, the page that a prefix ends in is the first sequence's, while the
-    others' own page holds NaN in the prefix's part."""
+    others' own page holds NaN in the prefix's part.  room: tokens that a table
+    row is wide enough for (long prefixes take another kernel, by that bound)."""
 
-    def __init__(self, seed, dtype, hq, hkv, d, page, new, held, groups=None, extra_rows=0, gap=0, values="normal"):
+    def __init__(self, seed, dtype, hq, hkv, d, page, new, held, groups=None, extra_rows=0, gap=0, values="normal",
+                 room=0):
         g = torch.Generator().manual_seed(seed)
         r = random.Random(seed)
         self.dtype, self.hq, self.hkv, self.d, self.page = dtype, hq, hkv, d, page
@@ -60,7 +62,7 @@ class Step:
                     prefix_of[b], first_of[b] = groups[1][x], groups[0][x]
         # a sequence's row covers what it holds; a group's first one covers the prefix too
         cover = [max(h, prefix_of[b] if first_of[b] == b else 0) for b, h in enumerate(held)]
-        width = max([1] + [-(-c // page) for c in cover])
+        width = max([1, room // page] + [-(-c // page) for c in cover])
         pages = sum(-(-c // page) for c in cover) + 3
         ids = list(range(pages))
         r.shuffle(ids)

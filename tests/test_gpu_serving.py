@@ -283,6 +283,48 @@ def test_paged_attention(name):
     _check(st, *_attend(st))
 
 
+def _room(hq, hkv, d, rows):
+    """Tokens of table room from which a group's prefix goes to the tensor-core kernel (2^30 of rows x Hkv x d x room)."""
+    return -(-(1 << 30) // (rows * hkv * d)) + 128
+
+
+GROUPED = [n for n, c in ATTEND_CASES.items()
+           if c[0] == BF16 and c[7] is not None and
+           max(sum(c[5][a:b]) for a, b in zip(c[7][0], c[7][0][1:])) * c[1] // c[2] > 32]
+
+
+@pytest.mark.parametrize("name", GROUPED)
+def test_paged_attention_with_room_for_long_prefixes(name):
+    """The same batches with wide tables, whose prefixes go to the tensor-core kernel."""
+    dt, hq, hkv, d, page, new, held, groups, values = ATTEND_CASES[name]
+    rows = sum(new) * hq // hkv
+    st = C.Step(len(name) + 1, dt, hq, hkv, d, page, new, held, groups, extra_rows=2, values=values,
+                room=_room(hq, hkv, d, rows))
+    a = _attend(st)
+    _check(st, *a)
+    for x, y in zip(a, _attend(st)):  # the same bits again
+        assert torch.equal(x, y)
+
+
+def test_long_prefix_reports_and_neighbours():
+    """A page outside the cache in a long prefix: reported, read as zeros; the other group's rows as they were."""
+    st = C.Step(31, BF16, 8, 1, 128, 16, [1] * 12, [150 + i for i in range(12)], ([0, 6, 12], [140, 150]),
+                room=_room(8, 1, 128, 96))
+    cache, batch, q = st.cache(), st.batch(), st.q.cuda()
+    att = api.PagedAttention(cache, batch, 8)
+    good = att(q, torch.empty_like(q)).clone()
+    assert att.status() == 0
+    for bad in (st.pages, -1, -2 ** 31, 2 ** 31 - 1):
+        batch.block_table[0, 3] = bad
+        out = att(q, torch.empty_like(q))
+        assert att.status() == 6
+        assert torch.equal(out[6:], good[6:]) and torch.isfinite(out).all()
+        att.reset()
+    batch.prefix_lens[0] = 10 ** 9
+    att(q, torch.empty_like(q))
+    assert att.status() == 6
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_paged_attention_scale_strides_and_page_gaps(dt):
     st = C.Step(4, dt, 8, 2, 128, 16, [2, 1, 3], [60, 200, 100], ([0, 3], [50]), gap=128, values="peaks")

@@ -255,6 +255,10 @@ def test_paged_attention_refusals():
     assert s.attend(q=_tok(4 * A + 4)) == INVALID and s.attend(out=_tok(8 * A, 520 // 8 * 8 + 4)) == INVALID
     assert s.attend(out=_tok(4 * A)) == INVALID and s.attend(out=_tok(4 * A + 1024)) == INVALID
     assert _Step(cu=[0, 2 ** 30, 2 ** 31 - 1]).size(hq=4)[0] == UNSUPPORTED
+    # more row and key tiles than the kernels count in 32 bits
+    many = _Step(cu=list(range(2049)), max_pages=2 ** 22, table_stride=2 ** 22)
+    assert many.size()[0] == UNSUPPORTED and many.attend(nbytes=1 << 40) == UNSUPPORTED
+    assert _Step(cu=list(range(2049)), max_pages=2 ** 13, table_stride=2 ** 13).size()[0] == OK
     assert _Step(cu=[0, 0, 0]).attend(q=NONE, out=NONE) == OK  # nothing to do
     assert _Step(cu=[0]).attend(q=NONE, out=NONE) == OK
 
