@@ -616,17 +616,21 @@ __global__ void __launch_bounds__(kFThreads)
 }
 
 // ------------------------------------------------------------------ join
-// One CTA for each (token, head): the partials of the row's prefix segment and
-// of its own segment, in the order of the CTAs that made them, dealt to four
-// warps, whose results join in the order of the warps.
-template <int D, typename T, int BN, int kMax>
+// The partials of a row (token, head): its prefix segment's and its own
+// segment's, in the order of the CTAs that made them.  WARPS warps take a row,
+// each a share of its partials, and join in the order of the warps: 4 where the
+// rows are few, so that a row's partials are all in flight at once, and 1 where they
+// are many, so that the CTAs are few enough to be there, their places
+// looked up, when the kernel before ends (2048 rows of 19 partials: 10.0 us
+// after its end with 4, 6.0 with 1; 128 rows: 2.8 with 4, 3.6 with 1).
+template <int D, typename T, int BN, int kMax, int WARPS>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
   constexpr int kCols = D / 32;
-  const int t = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x, h = blockIdx.y * (4 / WARPS) + warp / WARPS;
+  const int part = warp % WARPS;
   const int gh = w.by_group.d;
   const int b = paged_seq_of(w.p, t);
-  T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
   // a row's partials of one item: rows at + j * kStep for j < count
   struct Place {
     int seg, nt, ts, in_tile, j, n;  // segment, its key tiles, log2 rows a tile, row in the tile; item of its list, items
@@ -638,9 +642,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     const int g = w.by_group(h), r = (t - it.t0 - g) * gh + h;
     return Place{g * sp.rt + (r >> sp.ts), sp.nt, sp.ts, r & ((1 << sp.ts) - 1), i - l.begin, l.end - l.begin};
   };
+  constexpr int kPrefixRows = paged_prefix_rows(D);
   const bool own_list = w.prefix.end > 0;
   const int limit = paged_limit(w.p, b, t);
-  constexpr int kPrefixRows = paged_prefix_rows(D);
   Place pp{0, 0, 0, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
@@ -648,14 +652,10 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   }
   const Place po = place(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
   wait_for_previous();
-  if (limit <= 0) {
-    for (int c = threadIdx.x; c < D; c += 128) out[c] = static_cast<T>(0.f);
-    if (w.lse != nullptr && threadIdx.x == 0) w.lse[static_cast<long long>(t) * w.num_q_heads + h] = -INFINITY;
-    return;
-  }
+  const bool live = h < w.num_q_heads;
   auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> int {
     count = 0;
-    if (p.nt == 0) return 0;
+    if (p.nt == 0 || limit <= 0 || !live) return 0;
     const PagedCut cut{l.items[p.n], l.items[p.n + 1], l.by_ctas};
     const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt);
     const int row = l.items[p.n + 2 + p.j];
@@ -672,13 +672,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-  constexpr int kBatch = 4;  // partials in flight a warp
-  for (int j0 = warp; j0 < all; j0 += 4 * kBatch) {
+  constexpr int kBatch = WARPS == 4 || D == 256 ? 4 : 8;  // partials in flight a warp
+#pragma unroll 1
+  for (int j0 = part; j0 < all; j0 += WARPS * kBatch) {
     float2 ml[kBatch];
     float x[kBatch][kCols];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int j = j0 + 4 * i;
+      const int j = j0 + WARPS * i;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) x[i][c] = 0.f;
@@ -693,9 +694,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     }
     float top = m;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      top = fmaxf(top, ml[i].x);
-    }
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
     const float base = top == -INFINITY ? 0.f : top;
     const float f = ex2_approx(m - base);
     m = top;
@@ -710,31 +709,39 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
       for (int c = 0; c < kCols; ++c) acc[c] = fmaf(x[i][c], g, acc[c]);
     }
   }
-  __shared__ float acc_s[4][D];
-  __shared__ float2 ml_s[4];
+  if constexpr (WARPS == 4) {
+    __shared__ float acc_s[4][D];
+    __shared__ float2 ml_s[4];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
-  if (lane == 0) ml_s[warp] = make_float2(m, sum);
-  __syncthreads();
-  float top = -INFINITY;
+    for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
+    if (lane == 0) ml_s[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY, f[4];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) top = fmaxf(top, ml_s[x].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float f[4], l = 0.f;
+    for (int x = 0; x < 4; ++x) top = fmaxf(top, ml_s[x].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    sum = 0.f;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    f[x] = ex2_approx(ml_s[x].x - base);
-    l = fmaf(ml_s[x].y, f[x], l);
+    for (int x = 0; x < 4; ++x) {
+      f[x] = ex2_approx(ml_s[x].x - base);
+      sum = fmaf(ml_s[x].y, f[x], sum);
+    }
+    m = top;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      acc[c] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[c] = fmaf(acc_s[x][c * 32 + lane], f[x], acc[c]);
+    }
   }
-  const float inv = 1.f / l;
-  for (int c = threadIdx.x; c < D; c += 128) {
-    float a = 0.f;
+  if (!live) return;
+  T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
+  const float inv = limit > 0 ? 1.f / sum : 0.f;  // a row that sees no key: acc is 0
 #pragma unroll
-    for (int x = 0; x < 4; ++x) a = fmaf(acc_s[x][c], f[x], a);
-    out[c] = static_cast<T>(a * inv);
-  }
-  if (w.lse != nullptr && threadIdx.x == 0)
-    w.lse[static_cast<long long>(t) * w.num_q_heads + h] = (top + log2f(l)) * kLn2;
+  for (int c = 0; c < kCols; ++c) out[c * 32 + lane] = static_cast<T>(acc[c] * inv);
+  if (w.lse != nullptr && lane == 0)
+    w.lse[static_cast<long long>(t) * w.num_q_heads + h] = limit > 0 ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int sm_count() {
@@ -765,9 +772,15 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
 // CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
 
+constexpr int kFewRows = 1024;  // of the join, see there
+
 template <int D, typename T, int BN, int kMax>
 cudaError_t join(const PagedWork& w, cudaStream_t stream) {
-  return launch_after(paged_join_kernel<D, T, BN, kMax>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, true, w);
+  const long long rows = static_cast<long long>(w.p.total_q) * w.num_q_heads;
+  if (rows <= kFewRows)
+    return launch_after(paged_join_kernel<D, T, BN, kMax, 4>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, true, w);
+  return launch_after(paged_join_kernel<D, T, BN, kMax, 1>, dim3(w.p.total_q, (w.num_q_heads + 3) / 4), 128, 0, stream,
+                      true, w);
 }
 
 template <int D, int kMax>
