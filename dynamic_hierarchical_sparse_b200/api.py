@@ -532,28 +532,30 @@ def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dty
     tensor), on CUDA device `index`."""
     if t is None:
         return _NO_TOKENS
+    if t.ndim == 3:
+        n, h, d = t.shape
+        st, sh, sd = t.stride()
+        if (h == heads and d == head_dim and n >= tokens and sd == 1 and (sh == d or h == 1) and t.dtype is dtype
+                and t.get_device() == index):
+            return _Tokens(t.data_ptr(), st if n > 1 else h * d)
+    # what of it is wrong
     if t.get_device() != index:
         raise ValueError("%s must be a CUDA tensor on device %d, got %s" % (name, index, t.device))
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 3:
-        raise ValueError("%s must be [T, H, d], got %s" % (name, tuple(t.shape)))
-    n, h, d = t.shape
-    if n < tokens or h != heads or d != head_dim:
+    if t.ndim != 3 or n < tokens or h != heads or d != head_dim:
         raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(t.shape)))
-    st, sh, sd = t.stride()
-    if sd != 1 or (sh != head_dim and heads > 1):
-        raise ValueError("the heads of a token of %s must be contiguous" % name)
-    return _Tokens(t.data_ptr(), st if n > 1 else heads * head_dim)
+    raise ValueError("the heads of a token of %s must be contiguous" % name)
 
 
 def _int32(t: torch.Tensor, name: str, shape, index: int) -> None:
+    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
+        return
     if t.get_device() != index or index < 0:
         raise ValueError("%s must be a CUDA tensor on device %d" % (name, index))
     if t.dtype is not torch.int32:
         raise TypeError("%s must be int32" % name)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor, got %s" % (name, shape, tuple(t.shape)))
+    raise ValueError("%s must be a contiguous %s tensor, got %s" % (name, shape, tuple(t.shape)))
 
 
 class Rope:
@@ -569,7 +571,7 @@ class Rope:
                  inv_freq=None, factor: float = 1.0):
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.c = _RopeTable()
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.fn = ctypes.byref(self.c), lib().dhsa_rope
         if inv_freq is not None:
             f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
             if f.shape != (self.rotary_dim // 2,):
@@ -610,7 +612,7 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
             k_out = torch.empty(T, hk, d, dtype=dtype, device=x.device)
     if stream is not None:
         _enter(stream)
-    _call(lib().dhsa_rope, "dhsa_rope", dev, rope.ref, _dtype_code(x), d, T, positions.data_ptr(),
+    _call(rope.fn, "dhsa_rope", dev, rope.ref, _dtype_code(x), d, T, positions.data_ptr(),
           _tokens(q, "q", hq, d, dtype, T, dev), hq, _tokens(q_out, "q_out", hq, d, dtype, T, dev),
           _tokens(k, "k", hk, d, dtype, T, dev), hk, _tokens(k_out, "k_out", hk, d, dtype, T, dev),
           _stream_on(stream, dev))
