@@ -19,7 +19,8 @@
 // Q stays in registers, P goes from the S fragments straight into the A
 // operand of P V (f16, as V).
 //
-// paged_f32_kernel (fp32): the same list in FFMA, 32-key tiles by cp.async.
+// paged_f32_kernel (fp32): the same with 32-key tiles and 16 rows, on tf32
+// fragments in pairs.
 #include "launchers.h"
 #include "paged.cuh"
 
@@ -86,41 +87,176 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-struct MmaCtx {
+// A CTA's ring of key tiles (K, then V, in each stage) and where this warp is in it.
+struct Ring {
   uint32_t sbase, bar0;
   unsigned char* smem;
   volatile int* abort_flag;
   int stage;
   uint32_t phase;
+  template <int kStages>
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
-__device__ __forceinline__ uint32_t bar_full(const MmaCtx& c, int s) { return c.bar0 + 8u * s; }
+__device__ __forceinline__ uint32_t bar_full(const Ring& c, int s) { return c.bar0 + 8u * s; }
 template <int kStages>
-__device__ __forceinline__ uint32_t bar_empty(const MmaCtx& c, int s) {
+__device__ __forceinline__ uint32_t bar_empty(const Ring& c, int s) {
   return c.bar0 + 8u * (kStages + s);
 }
 
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The producer warp: brings the key tiles of all the CTA's pieces into the ring,
+// by slices of kCols columns (128 bytes, swizzled), a lane for each box (page
+// part, slice, K or V).
+template <int BN, int kCols, int kSlices, int kStages, typename Walk>
+__device__ __forceinline__ void page_producer(const PagedWork& w, Walk& walk, const CUtensorMap* tm_k,
+                                              const CUtensorMap* tm_v, Ring& ring) {
+  constexpr int kTileBytes = kSlices * BN * 128;
+  const int lane = threadIdx.x & 31;
+  const int ps = w.p.page_size, psh = w.p.page_shift;
+  const int box = ps < BN ? ps : BN;
+  const int kv = lane & 1, sl = (lane >> 1) % kSlices, pp = (lane >> 1) / kSlices;
+  const bool mine = pp * box < BN;
+  const CUtensorMap* map = kv ? tm_v : tm_k;
+  const uint32_t dst0 = ring.sbase + kv * kTileBytes + sl * (BN * 128) + pp * box * 128;
+  int issued = 0;
+  bool ok = true;
+  do {
+    const int h = walk.h;
+    const int* table = w.p.block_table + static_cast<long long>(walk.it.row) * w.p.table_stride;
+    // the page of this lane's part of a tile, -1 where the item has no key in it
+    auto page_at = [&](int kt) -> int {
+      const int key = (walk.first + walk.kt + kt) * BN + pp * box;
+      if (kt >= walk.count || !mine || key >= walk.it.hi || key + box <= walk.it.lo) return -1;
+      const int pg = table[key >> psh];
+      if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) return pg;
+      report(w.status, kDevCheck);
+      return w.p.num_pages;  // outside the map: the box arrives as zeros
+    };
+    int page = page_at(0);
+    for (int kt = 0; kt < walk.count; ++kt) {
+      const int page_next = page_at(kt + 1);
+      const int s = ring.stage;
+      if (issued >= kStages) ok = mbar_wait(bar_empty<kStages>(ring, s), ring.phase ^ 1u, ring.abort_flag, w.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const unsigned active = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, s), __popc(active) * box * 128);
+      __syncwarp();
+      if (page >= 0) {
+        const int key = (walk.first + walk.kt + kt) * BN + pp * box;
+        tma_load_4d(dst0 + s * 2 * kTileBytes, map, bar_full(ring, s), sl * kCols, key & (ps - 1), h, page);
+      }
+      ++issued;
+      page = page_next;
+      ring.template next<kStages>();
+    }
+  } while (ok && walk.next());
+  if (*ring.abort_flag && lane == 0) {
+    // let copies already in flight land before the CTA exits (bounded)
+    volatile int never = 0;
+    for (int x = max(0, issued - kStages); x < issued; ++x)
+      mbar_wait(bar_full(ring, x % kStages), (x / kStages) & 1, &never, nullptr, 10000000ull);
+  }
+}
 
-// The same barrier, and whether any of the 128 threads says so: every warp
-// takes the same way out.
+// A barrier of the compute warps (N threads), and the same saying whether any of
+// the threads says so: every warp takes the same way out.
+template <int N>
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ bool compute_sync_or(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u)
+      : "r"(x ? 1u : 0u), "n"(N)
       : "memory");
   return r != 0;
+}
+
+// The end of a piece on the four compute warps: joins the WN warps of each row
+// group, a quarter of the columns at a time, in the order of the warps, and
+// leaves the piece's partial.  o: m16n8 fragments of the warp's 16 rows.  false:
+// a warp's wait gave up.
+template <int D, typename C, int kMax, int WM, int WN, typename Walk>
+__device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, const Ring& ctx, float (&o)[D / 8][4],
+                                             const float (&m)[2], float (&l)[2], bool ok) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wm = warp / WN;
+  float* join = reinterpret_cast<float*>(ctx.smem + C::kOffJoin);
+  float2* ml = reinterpret_cast<float2*>(ctx.smem + C::kOffMl);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    if ((lane & 3) == 0) ml[warp * 16 + (lane >> 2) + 8 * e] = make_float2(m[e], l[e]);
+  }
+  compute_sync<128>();
+  float f[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
+    f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
+  }
+  const int part = paged_part_row(blockIdx.x, kMax, k.item_row, k.seg(), k.ts);
+  const int valid = min(k.rows() - k.row0(), WM * 16);
+  if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
+    const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(g * WN + x) * 16 + r].x);
+#pragma unroll
+    for (int x = 0; x < WN; ++x) {
+      const float2 v = ml[(g * WN + x) * 16 + r];
+      sum += v.y * (top == -INFINITY ? 1.f : ex2_approx(v.x - top));
+    }
+    w.list.part_ml[part + threadIdx.x] = make_float2(top, sum);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const int jj = c * (D / 32) + j;
+      float* dst = join + (warp * 16 + (lane >> 2)) * C::kJoinStride + 8 * j + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(dst) = make_float2(o[jj][0] * f[0], o[jj][1] * f[0]);
+      *reinterpret_cast<float2*>(dst + 8 * C::kJoinStride) = make_float2(o[jj][2] * f[1], o[jj][3] * f[1]);
+    }
+    compute_sync<128>();
+    constexpr int kVecs = D / 16;  // float4s of a row's quarter
+    for (int x = threadIdx.x; x < valid * kVecs; x += 128) {
+      const int r = x / kVecs, v = x % kVecs;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int y = 0; y < WN; ++y) {
+        const float4 u = *reinterpret_cast<const float4*>(
+            join + (((r >> 4) * WN + y) * 16 + (r & 15)) * C::kJoinStride + 4 * v);
+        a.x += u.x;
+        a.y += u.y;
+        a.z += u.z;
+        a.w += u.w;
+      }
+      *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + c * (D / 4) + 4 * v) = a;
+    }
+    if (c < 3) compute_sync<128>();
+  }
+  return !compute_sync_or<128>(!ok);
 }
 
 // One piece on the four compute warps: WM warps along the rows, WN along a
 // tile's keys.  false: a warp's wait gave up.
 template <int D, int kMax, int WM, int WN>
-__device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kBN, kMax>& k, MmaCtx& ctx) {
+__device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kBN, kMax>& k, Ring& ctx) {
   using C = MmaCfg<D>;
   constexpr int kWarpKeys = kBN / WN;
   constexpr int kSub = WN == 4 ? 16 : (D == 256 ? 16 : 32);  // keys of one softmax step
@@ -284,73 +420,37 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_empty<C::kStages>(ctx, ctx.stage));
-    if (++ctx.stage == C::kStages) {
-      ctx.stage = 0;
-      ctx.phase ^= 1u;
-    }
+    ctx.template next<C::kStages>();
   }
 
-  // join the WN warps of each row group, a quarter of the columns at a time,
-  // in the order of the warps
-  float* join = reinterpret_cast<float*>(ctx.smem + C::kOffJoin);
-  float2* ml = reinterpret_cast<float2*>(ctx.smem + C::kOffMl);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    if ((lane & 3) == 0) ml[warp * 16 + (lane >> 2) + 8 * e] = make_float2(m[e], l[e]);
-  }
-  compute_sync();
-  float f[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(wm * WN + x) * 16 + (lane >> 2) + 8 * e].x);
-    f[e] = top == -INFINITY ? 1.f : ex2_approx(m[e] - top);
-  }
-  const int part = paged_part_row(blockIdx.x, kMax, k.item_row, k.seg(), k.ts);
-  const int valid = min(rows - row0, WM * 16);
-  if (threadIdx.x < WM * 16 && static_cast<int>(threadIdx.x) < valid) {
-    const int g = threadIdx.x >> 4, r = threadIdx.x & 15;
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int x = 0; x < WN; ++x) top = fmaxf(top, ml[(g * WN + x) * 16 + r].x);
-#pragma unroll
-    for (int x = 0; x < WN; ++x) {
-      const float2 v = ml[(g * WN + x) * 16 + r];
-      sum += v.y * (top == -INFINITY ? 1.f : ex2_approx(v.x - top));
+  return finish_piece<D, C, kMax, WM, WN>(w, k, ctx, o, m, l, ok);
+}
+
+// The start of a list's kernel: the ring's barriers and the CTA's first piece.
+// false (for the whole CTA): no work.
+template <typename C, int BN, int kMax>
+__device__ __forceinline__ bool open_list(const PagedWork& w, unsigned char* smem_raw, Ring& ctx,
+                                          PagedWalk<BN, kMax>& walk) {
+  ctx.smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  ctx.sbase = smem_u32(ctx.smem);
+  ctx.bar0 = ctx.sbase + C::kOffBar;
+  ctx.abort_flag = reinterpret_cast<volatile int*>(ctx.smem + C::kOffBar + 8 * 2 * C::kStages);
+  ctx.stage = 0;
+  ctx.phase = 0;
+  PagedScan* sc = reinterpret_cast<PagedScan*>(ctx.smem + C::kOffScan);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_full(ctx, s), 1);
+      mbar_init(bar_empty<C::kStages>(ctx, s), 4);
     }
-    w.list.part_ml[part + threadIdx.x] = make_float2(top, sum);
+    *ctx.abort_flag = 0;
+    fence_mbar_init();
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const int jj = c * (D / 32) + j;
-      float* dst = join + (warp * 16 + (lane >> 2)) * C::kJoinStride + 8 * j + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(dst) = make_float2(o[jj][0] * f[0], o[jj][1] * f[0]);
-      *reinterpret_cast<float2*>(dst + 8 * C::kJoinStride) = make_float2(o[jj][2] * f[1], o[jj][3] * f[1]);
-    }
-    compute_sync();
-    constexpr int kVecs = D / 16;  // float4s of a row's quarter
-    for (int x = threadIdx.x; x < valid * kVecs; x += 128) {
-      const int r = x / kVecs, v = x % kVecs;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int y = 0; y < WN; ++y) {
-        const float4 u = *reinterpret_cast<const float4*>(
-            join + (((r >> 4) * WN + y) * 16 + (r & 15)) * C::kJoinStride + 4 * v);
-        a.x += u.x;
-        a.y += u.y;
-        a.z += u.z;
-        a.w += u.w;
-      }
-      *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + c * (D / 4) + 4 * v) = a;
-    }
-    if (c < 3) compute_sync();
-  }
-  return !compute_sync_or(!ok);
+  paged_schedule<BN, kMax, kMmaThreads, 0>(w.p, w.by_group.d, w.list, sc, w.status);
+  __syncthreads();
+  let_next_start();
+  return walk.init(&w.p, w.by_group.d, w.list, sc);
 }
 
 // kMax: rows a tile at most, 64, or 16 for a list without more (decode steps
@@ -361,90 +461,18 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
                      const __grid_constant__ PagedWork w) {
   using C = MmaCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  MmaCtx ctx;
-  ctx.smem = smem;
-  ctx.sbase = smem_u32(smem);
-  ctx.bar0 = ctx.sbase + C::kOffBar;
-  ctx.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * 2 * C::kStages);
-  ctx.stage = 0;
-  ctx.phase = 0;
-  PagedScan* sc = reinterpret_cast<PagedScan*>(smem + C::kOffScan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.by_group.d;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar_full(ctx, s), 1);
-      mbar_init(bar_empty<C::kStages>(ctx, s), 4);
-    }
-    *ctx.abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == kProducer && lane == 0) {
+  Ring ctx;
+  PagedWalk<kBN, kMax> walk;
+  if (threadIdx.x == 32 * kProducer) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  paged_schedule<kBN, kMax, kMmaThreads, 0>(w.p, gh, w.list, sc, w.status);
-  __syncthreads();
-
-  let_next_start();
-  PagedWalk<kBN, kMax> walk;
-  if (!walk.init(&w.p, gh, w.list, sc)) {  // uniform for the CTA
+  if (!open_list<C, kBN, kMax>(w, smem_raw, ctx, walk)) {
     wait_for_previous();
     return;
   }
-
-  if (warp == kProducer) {
-    // a lane for each box of a tile: (page part, 64-column slice, K or V)
-    const int ps = w.p.page_size, psh = w.p.page_shift;
-    const int box = ps < kBN ? ps : kBN;
-    const int kv = lane & 1, sl = (lane >> 1) % C::kSlices, pp = (lane >> 1) / C::kSlices;
-    const bool mine = pp * box < kBN;
-    const CUtensorMap* map = kv ? &tm_v : &tm_k;
-    const uint32_t dst0 = ctx.sbase + kv * C::kTileBytes + sl * (kBN * 128) + pp * box * 128;
-    int issued = 0;
-    bool ok = true;
-    do {
-      const int h = walk.h;
-      const int* table = w.p.block_table + static_cast<long long>(walk.it.row) * w.p.table_stride;
-      // the page of this lane's part of a tile, -1 where the item has no key in it
-      auto page_at = [&](int kt) -> int {
-        const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
-        if (kt >= walk.count || !mine || key >= walk.it.hi || key + box <= walk.it.lo) return -1;
-        const int pg = table[key >> psh];
-        if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) return pg;
-        report(w.status, kDevCheck);
-        return w.p.num_pages;  // outside the map: the box arrives as zeros
-      };
-      int page = page_at(0);
-      for (int kt = 0; kt < walk.count; ++kt) {
-        const int page_next = page_at(kt + 1);
-        const int s = ctx.stage;
-        if (issued >= C::kStages) ok = mbar_wait(bar_empty<C::kStages>(ctx, s), ctx.phase ^ 1u, ctx.abort_flag, w.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const unsigned active = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(bar_full(ctx, s), __popc(active) * box * 128);
-        __syncwarp();
-        if (page >= 0) {
-          const int key = (walk.first + walk.kt + kt) * kBN + pp * box;
-          tma_load_4d(dst0 + s * 2 * C::kTileBytes, map, bar_full(ctx, s), sl * 64, key & (ps - 1), h, page);
-        }
-        ++issued;
-        page = page_next;
-        if (++ctx.stage == C::kStages) {
-          ctx.stage = 0;
-          ctx.phase ^= 1u;
-        }
-      }
-    } while (ok && walk.next());
-    if (*ctx.abort_flag && lane == 0) {
-      // let copies already in flight land before the CTA exits (bounded)
-      volatile int never = 0;
-      for (int x = max(0, issued - C::kStages); x < issued; ++x)
-        mbar_wait(bar_full(ctx, x % C::kStages), (x / C::kStages) & 1, &never, nullptr, 10000000ull);
-    }
+  if (threadIdx.x / 32 == kProducer) {
+    page_producer<kBN, 64, C::kSlices, C::kStages>(w, walk, &tm_k, &tm_v, ctx);
   } else {
     bool ok;
     do {
@@ -459,160 +487,217 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 }
 
 // ------------------------------------------------------------------ fp32
+// fp32 products on tf32 fragments, each number as the sum of two: x = h + l with
+// h the tf32 (11 bits) nearest to x and l the tf32 nearest to x - h, so h + l is
+// x to 2^-22, and a b = h h' + h l' + l h' to about 2^-21 of |a b|, accumulated in
+// fp32.  (The same in FFMA is bound by shared memory: 16 rows are too few for a
+// register block that would feed it.)  A tile is 16 rows and 32 keys; the four
+// warps split the keys.
 constexpr int kFBN = 32;    // keys a tile
 constexpr int kFRows = 16;  // rows a tile
-constexpr int kFThreads = 128;
 
 template <int D>
 struct F32Cfg {
-  static constexpr int kStride = D + 4;  // floats; + 4: 16-byte reads of consecutive rows hit all banks
-  static constexpr int kTile = kFBN * kStride;
-  static constexpr int kOffQ = 2 * 2 * kTile * 4;
-  static constexpr int kOffP = kOffQ + kFRows * D * 4;
-  static constexpr int kOffScan = kOffP + kFBN * kFRows * 4;
-  static constexpr int kSmemBytes = kOffScan + static_cast<int>(sizeof(PagedScan));
+  static constexpr int kSlices = D / 32;  // 32-column (128-byte) slices of a row
+  static constexpr int kTileBytes = kFBN * D * 4;
+  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kCtas = D == 64 ? 3 : D == 128 ? 2 : 1;  // resident on an SM
+  static constexpr int kQStride = D + 4;  // floats; + 4: 16-byte reads of 8 rows hit all banks
+  static constexpr int kJoinStride = D / 4 + 8;
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;           // h, then l of Q
+  static constexpr int kOffJoin = kOffQ + 2 * kFRows * kQStride * 4;
+  static constexpr int kOffMl = kOffJoin + 4 * 16 * kJoinStride * 4;
+  static constexpr int kOffScan = kOffMl + 4 * 16 * 8;
+  static constexpr int kOffBar = kOffScan + ((static_cast<int>(sizeof(PagedScan)) + 15) / 16) * 16;
+  static constexpr int kSmemBytes = kOffBar + 8 * 2 * kStages + 16 + 1024;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& h, uint32_t& l) {
+  h = to_tf32(x);
+  l = to_tf32(x - __uint_as_float(h));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One piece on the four compute warps.
 template <int D>
-__global__ void __launch_bounds__(kFThreads)
-    paged_f32_kernel(const __grid_constant__ PagedWork w) {
+__device__ __forceinline__ bool f32_piece(const PagedWork& w, const PagedWalk<kFBN, kFRows>& k, Ring& ctx) {
+  using C = F32Cfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gh = k.group_heads, h = k.h, rows = k.rows(), row0 = k.row0();
+  const float scale_log2 = w.scale * kLog2e;
+  uint32_t* qh = reinterpret_cast<uint32_t*>(ctx.smem + C::kOffQ);
+  uint32_t* ql = qh + kFRows * C::kQStride;
+  // (the previous piece's last barrier is behind its reads of Q)
+#pragma unroll 4
+  for (int x = threadIdx.x; x < kFRows * (D / 4); x += 128) {
+    const int tr = x / (D / 4), c = x % (D / 4), r = row0 + tr;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      const int t = w.by_group(r);
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(w.q) + (k.it.t0 + t) * w.q_stride +
+                                           static_cast<long long>((h - t) * gh + r) * D + 4 * c);
+    }
+    uint4 vh, vl;
+    split_tf32(v.x, vh.x, vl.x);
+    split_tf32(v.y, vh.y, vl.y);
+    split_tf32(v.z, vh.z, vl.z);
+    split_tf32(v.w, vh.w, vl.w);
+    *reinterpret_cast<uint4*>(qh + tr * C::kQStride + 4 * c) = vh;
+    *reinterpret_cast<uint4*>(ql + tr * C::kQStride + 4 * c) = vl;
+  }
+  int lim[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = row0 + (lane >> 2) + 8 * e;
+    lim[e] = 0;
+    if (r < rows) {
+      const int t = k.it.t0 + w.by_group(r);
+      const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
+      lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
+    }
+  }
+  float o[D / 8][4];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const int r0 = 8 * warp;  // the warp's first key within a tile
+  const int key7 = lane & 7;
+  const uint32_t qa = smem_u32(qh) + (((lane & 7) + ((lane >> 3) & 1) * 8) * C::kQStride + (lane >> 4) * 4) * 4;
+  constexpr uint32_t kLow = kFRows * C::kQStride * 4;
+  compute_sync<128>();  // Q is there
+  bool ok = true;  // a warp whose wait gave up still takes part in the barriers at the end
+  for (int kt = 0; kt < k.count; ++kt) {
+    ok = mbar_wait(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag, w.status);
+    if (!ok) break;
+    const uint32_t sk = ctx.sbase + ctx.stage * 2 * C::kTileBytes, sv = sk + C::kTileBytes;
+    const int key0 = (k.first + k.kt + kt) * kFBN + r0;
+    // six independent sums (products of h, and both kinds of cross products, of
+    // even and odd steps): one chain of dependent MMAs would be all latency
+    float sh[2][4], sx[2][4], sy[2][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[e >> 2][e & 3] = sx[e >> 2][e & 3] = sy[e >> 2][e & 3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {  // 16 columns
+      uint32_t kr[4];
+      const int chunk = (ks * 4 + (lane >> 3)) & 7;
+      ldsm4(kr, sk + (ks >> 1) * (kFBN * 128) + (r0 + key7) * 128 + ((chunk ^ key7) << 4));
+      uint32_t kh[4], kl[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(kr[e]), kh[e], kl[e]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t ah[4], al[4];
+        ldsm4(ah, qa + (ks * 16 + half * 8) * 4);
+        ldsm4(al, qa + kLow + (ks * 16 + half * 8) * 4);
+        mma_tf32(sx[half], ah, kl[2 * half], kl[2 * half + 1]);
+        mma_tf32(sh[half], ah, kh[2 * half], kh[2 * half + 1]);
+        mma_tf32(sy[half], al, kh[2 * half], kh[2 * half + 1]);
+      }
+    }
+    const int q2 = 2 * (lane & 3);
+    float s[4], mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = key0 + q2 + (e & 1);
+      const float dot = (sh[0][e] + sh[1][e]) + ((sx[0][e] + sx[1][e]) + (sy[0][e] + sy[1][e]));
+      s[e] = key < k.it.lo || key >= lim[e >> 1] ? -INFINITY : dot * scale_log2;
+      mx[e >> 1] = fmaxf(mx[e >> 1], s[e]);
+    }
+    bool grew = false;
+    float mnew[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+      mnew[e] = fmaxf(m[e], mx[e]);
+      grew |= mnew[e] > m[e];
+    }
+    if (__any_sync(0xffffffffu, grew)) {
+      float al[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        al[e] = mnew[e] > m[e] ? ex2_approx(m[e] - mnew[e]) : 1.f;
+        m[e] = mnew[e];
+        l[e] *= al[e];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] *= al[0];
+        o[j][1] *= al[0];
+        o[j][2] *= al[1];
+        o[j][3] *= al[1];
+      }
+    }
+    // P as the A operand: k index q of the fragment stands for key 2q, q + 4 for key 2q + 1
+    uint32_t ph[4], pl[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = ex2_approx(s[e] - (m[e >> 1] == -INFINITY ? 0.f : m[e >> 1]));
+      l[e >> 1] += x;
+      split_tf32(x, ph[(e & 1) * 2 + (e >> 1)], pl[(e & 1) * 2 + (e >> 1)]);
+    }
+    // slots that hold no key of this item may hold anything, NaN included: taken as zero
+    const bool keep0 = key0 + q2 >= k.it.lo && key0 + q2 < k.it.hi;
+    const bool keep1 = key0 + q2 + 1 >= k.it.lo && key0 + q2 + 1 < k.it.hi;
+    const int row_a = q2, row_b = q2 + 1;  // (r0 is a multiple of 8: the swizzle goes by these alone)
+    const int g = lane >> 2;
+#pragma unroll
+    for (int j0 = 0; j0 < D / 8; j0 += 4) {  // four 8-column blocks of O between dependent MMAs
+      uint32_t vh[4][2], vl[4][2];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = j0 + x;
+        const int chunk = (2 * j + (g >> 2)) & 7;
+        const uint32_t at = sv + (j >> 2) * (kFBN * 128) + r0 * 128 + (g & 3) * 4;
+        float v0, v1;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v0) : "r"(at + row_a * 128 + ((chunk ^ row_a) << 4)) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v1) : "r"(at + row_b * 128 + ((chunk ^ row_b) << 4)) : "memory");
+        split_tf32(keep0 ? v0 : 0.f, vh[x][0], vl[x][0]);
+        split_tf32(keep1 ? v1 : 0.f, vh[x][1], vl[x][1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma_tf32(o[j0 + x], ph, vl[x][0], vl[x][1]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma_tf32(o[j0 + x], pl, vh[x][0], vh[x][1]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma_tf32(o[j0 + x], ph, vh[x][0], vh[x][1]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty<C::kStages>(ctx, ctx.stage));
+    ctx.template next<C::kStages>();
+  }
+  return finish_piece<D, C, kFRows, 1, 4>(w, k, ctx, o, m, l, ok);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
+    paged_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ PagedWork w) {
   using C = F32Cfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  float* kv = reinterpret_cast<float*>(smem_raw);
-  float* qs = reinterpret_cast<float*>(smem_raw + C::kOffQ);  // [row][D]
-  float* ps = reinterpret_cast<float*>(smem_raw + C::kOffP);  // [warp][key][4 rows]
-  PagedScan* sc = reinterpret_cast<PagedScan*>(smem_raw + C::kOffScan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gh = w.by_group.d;
-  paged_schedule<kFBN, kFRows, kFThreads, 0>(w.p, gh, w.list, sc, w.status);
-  __syncthreads();
-  let_next_start();
-  PagedWalk<kFBN, kFRows> k;
-  if (!k.init(&w.p, gh, w.list, sc)) return;
-  const float scale_log2 = w.scale * kLog2e;
-  do {
-    const int h = k.h, rows = k.rows(), row0 = k.row0();
-    const int* table = w.p.block_table + static_cast<long long>(k.it.row) * w.p.table_stride;
-    auto fetch = [&](int kt) {
-      const int buf = kt & 1;
-      const int tile0 = (k.first + k.kt + kt) * kFBN;
-      for (int x = threadIdx.x; x < kFBN * (D / 4); x += kFThreads) {
-        const int r = x / (D / 4), c = x % (D / 4);
-        const int key = tile0 + r;
-        bool take = key >= k.it.lo && key < k.it.hi;
-        long long off = 0;
-        if (take) {
-          const int pg = table[key >> w.p.page_shift];
-          if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages)) {
-            off = pg * w.p.page_stride + (static_cast<long long>(h) * w.p.page_size + (key & (w.p.page_size - 1))) * D + 4 * c;
-          } else {
-            take = false;  // taken as zeros
-            report(w.status, kDevCheck);
-          }
-        }
-        const uint32_t dst = smem_u32(kv + (buf * 2) * C::kTile + r * C::kStride + 4 * c);
-        cp_async16(dst, static_cast<const float*>(w.p.k_pages) + off, take);
-        cp_async16(dst + C::kTile * 4, static_cast<const float*>(w.p.v_pages) + off, take);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    __syncthreads();  // the previous piece is read out
-    fetch(0);
-    for (int x = threadIdx.x; x < kFRows * (D / 4); x += kFThreads) {
-      const int r = row0 + x / (D / 4), c = x % (D / 4);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows) {
-        const int tr = w.by_group(r);
-        v = *reinterpret_cast<const float4*>(static_cast<const float*>(w.q) + (k.it.t0 + tr) * w.q_stride +
-                                             static_cast<long long>((h - tr) * gh + r) * D + 4 * c);
-      }
-      *reinterpret_cast<float4*>(qs + (x / (D / 4)) * D + 4 * c) = v;
+  Ring ctx;
+  PagedWalk<kFBN, kFRows> walk;
+  if (!open_list<C, kFBN, kFRows>(w, smem_raw, ctx, walk)) return;
+  if (threadIdx.x / 32 == kProducer) {
+    page_producer<kFBN, 32, C::kSlices, C::kStages>(w, walk, &tm_k, &tm_v, ctx);
+  } else {
+    while (f32_piece<D>(w, walk, ctx) && walk.next()) {
     }
-    // warp w has rows 4w .. 4w + 3
-    int lim[4];
-    float m[4], l[4];
-    constexpr int kCols = D / 32;  // columns of a lane
-    float o[4][kCols];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = row0 + warp * 4 + e;
-      lim[e] = 0;
-      if (r < rows) {
-        const int t = k.it.t0 + w.by_group(r);
-        const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
-        lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
-      }
-      m[e] = -INFINITY;
-      l[e] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) o[e][c] = 0.f;
-    }
-    for (int kt = 0; kt < k.count; ++kt) {
-      if (kt + 1 < k.count) {
-        fetch(kt + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-      __syncthreads();
-      const float* ks = kv + (kt & 1) * 2 * C::kTile;
-      const float* vs = ks + C::kTile;
-      const int key = (k.first + k.kt + kt) * kFBN + lane;  // a lane has one key
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int c = 0; c < D; c += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(ks + lane * C::kStride + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 b = *reinterpret_cast<const float4*>(qs + (warp * 4 + e) * D + c);
-          s[e] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[e]))));
-        }
-      }
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = key < k.it.lo || key >= lim[e] ? -INFINITY : s[e] * scale_log2;
-        float mx = x;
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m[e], mx);
-        const float al = mn > m[e] ? ex2_approx(m[e] - mn) : 1.f;
-        m[e] = mn;
-        p[e] = ex2_approx(x - (mn == -INFINITY ? 0.f : mn));
-        l[e] = l[e] * al + p[e];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) o[e][c] *= al;
-      }
-      *reinterpret_cast<float4*>(ps + (warp * kFBN + lane) * 4) = make_float4(p[0], p[1], p[2], p[3]);
-      __syncwarp();
-#pragma unroll 4
-      for (int j = 0; j < kFBN; ++j) {
-        const float4 pj = *reinterpret_cast<const float4*>(ps + (warp * kFBN + j) * 4);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const float v = vs[j * C::kStride + c * 32 + lane];
-          o[0][c] = fmaf(pj.x, v, o[0][c]);
-          o[1][c] = fmaf(pj.y, v, o[1][c]);
-          o[2][c] = fmaf(pj.z, v, o[2][c]);
-          o[3][c] = fmaf(pj.w, v, o[3][c]);
-        }
-      }
-      __syncthreads();  // the buffer is free for the tile after next
-    }
-    const int part = paged_part_row(blockIdx.x, kFRows, k.item_row, k.seg(), k.ts);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float sum = l[e];
-#pragma unroll
-      for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const int r = warp * 4 + e;
-      if (row0 + r < rows) {
-        if (lane == 0) w.list.part_ml[part + r] = make_float2(m[e], sum);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) w.list.part_o[static_cast<long long>(part + r) * D + c * 32 + lane] = o[e][c];
-      }
-    }
-  } while (k.next());
+  }
 }
 
 // ------------------------------------------------------------------ join
@@ -787,8 +872,8 @@ template <int D, int kMax>
 cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   using C = MmaCfg<D>;
   CUtensorMap mk, mv;
-  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, false) != CUDA_SUCCESS ||
-      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, true) != CUDA_SUCCESS)
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, kMax>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -807,13 +892,16 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
 template <int D>
 cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   using C = F32Cfg<D>;
+  CUtensorMap mk, mv;
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, kFBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT32) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, kFBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT32) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int per_sm = D == 256 ? 1 : D == 128 ? 2 : 3;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  w.list.by_ctas = FastDiv(sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas);
-  paged_f32_kernel<D><<<w.list.by_ctas.d, kFThreads, C::kSmemBytes, stream>>>(w);
+  w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
+  paged_f32_kernel<D><<<w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return join<D, float, kFBN, kFRows>(w, stream);
@@ -821,20 +909,21 @@ cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
 
 }  // namespace
 
-// (d, page_size, Hkv, pages) view of a 16-bit page array; one box is 64 columns
-// of up to `tile` tokens of a page, rows of 128 bytes, swizzled.
-CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16) {
+// (d, page_size, Hkv, pages) view of a page array; one box is 128 bytes of up
+// to `tile` tokens of a page, as rows of 128 bytes, swizzled.
+CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile,
+                          CUtensorMapDataType type) {
   const TensorMapEncodeFn fn = tensor_map_encode_fn();
   if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t bytes = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.page_size),
                               static_cast<cuuint64_t>(p.num_kv_heads), static_cast<cuuint64_t>(p.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.head_dim) * 2,
-                                 static_cast<cuuint64_t>(p.page_size) * p.head_dim * 2,
-                                 static_cast<cuuint64_t>(p.page_stride) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page_size < tile ? p.page_size : tile), 1, 1};
+  const cuuint64_t strides[3] = {p.head_dim * bytes, static_cast<cuuint64_t>(p.page_size) * p.head_dim * bytes,
+                                 static_cast<cuuint64_t>(p.page_stride) * bytes};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / bytes),
+                             static_cast<cuuint32_t>(p.page_size < tile ? p.page_size : tile), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return fn(map, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

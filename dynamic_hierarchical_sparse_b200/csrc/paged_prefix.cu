@@ -617,8 +617,8 @@ template <int D>
 cudaError_t run(const PagedWork& w, cudaStream_t stream) {
   using C = PrefixCfg<D>;
   CUtensorMap mk, mv;
-  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, false) != CUDA_SUCCESS ||
-      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, true) != CUDA_SUCCESS)
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaError_t e =
       cudaFuncSetAttribute(paged_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);

@@ -107,8 +107,8 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
 
 cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, int dtype, cudaStream_t stream);
 
-// TMA view of a 16-bit page array; one box is 64 columns of up to `tile` tokens of a page.
-CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, bool f16);
+// TMA view of a page array; one box is 128 bytes of up to `tile` tokens of a page.
+CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, CUtensorMapDataType type);
 
 // The prefixes' list on tcgen05 (bf16): key tiles of 128, row tiles of up to
 // 256 (128 for d 256), one CTA an SM.
