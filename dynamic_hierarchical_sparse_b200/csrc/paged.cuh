@@ -116,16 +116,19 @@ struct PagedSpan {
   }
 };
 
-// How a list's key tiles (units, fewer than 2^30) are cut among the CTAs.
-// chunk 0: evenly, wherever that falls; with fewer units than CTAs the first
-// `total` CTAs take one each, so every CTA between the first and the last owner
-// of a segment has a partial of it.  chunk > 0: every segment counts as a whole
-// number of chunks, a CTA takes one chunk, and none has two segments.
+// How a list's units (fewer than 2^30) are cut among the CTAs.  chunk 0: a
+// segment counts its key tiles and `extra` units behind them, for what its
+// start and end cost (none where there are no more tiles than CTAs), and the
+// units are cut evenly, wherever that falls; with fewer units than CTAs the
+// first `total` CTAs take one each, so every CTA between the owners of a
+// segment's first and last tile has a partial of it.
+// chunk > 0: every segment counts as a whole number of chunks, a CTA takes one
+// chunk, and none has two segments.
 struct PagedCut {
-  int total, chunk;
+  int total, chunk, extra;
   FastDiv by_ctas;
-  __device__ __forceinline__ int padded(int nt) const {
-    return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt;
+  __device__ __forceinline__ int padded(int nt) const {  // a segment's units
+    return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt > 0 ? nt + extra : 0;
   }
   __device__ __forceinline__ int first(int c) const {  // the first unit of CTA c: c * total / ctas
     if (chunk > 0) return min(c * chunk, total);
@@ -176,7 +179,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
   const int i0 = min(thread * per, n), i1 = min(i0 + per, n);
   const int lane = thread & 31, warp = thread >> 5;
   auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-  PagedCut cut{0, 0, list.by_ctas};
+  PagedCut cut{0, 0, 0, list.by_ctas};
   int base_u = 0, base_r = 0;
   // rounds (one body, so that its code comes in once): the plain count with
   // its segments (kSnap), the padded count, then the finding of this CTA's item
@@ -219,35 +222,39 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     }
     if (find) break;
     if (bad) report(status, kDevCheck);
-    int iu = units, ir = rows;
+    int iu = units, ir = rows, is = segs;
 #pragma unroll 1
     for (int o = 1; o < 32; o *= 2) {
       const int u = __shfl_up_sync(0xffffffffu, iu, o), r = __shfl_up_sync(0xffffffffu, ir, o);
+      const int g = __shfl_up_sync(0xffffffffu, is, o);
       if (lane >= o) {
         iu += u;
         ir += r;
+        is += g;
       }
     }
-    if (kSnap > 0 && round == 0) segs = __reduce_add_sync(0xffffffffu, segs);
     if (lane == 31) {
       sc->warp_units[warp] = iu;
       sc->warp_rows[warp] = ir;
-      sc->warp_segs[warp] = segs;
+      sc->warp_segs[warp] = is;
     }
     meet();
     base_u = iu - units;
     base_r = ir - rows;
+    const int mine_s = segs;
+    int base_s = is - segs;
     cut.total = 0;
     segs = 0;
 #pragma unroll 1
     for (int x = 0; x < kThreads / 32; ++x) {
-      const int u = sc->warp_units[x];
+      const int u = sc->warp_units[x], g = sc->warp_segs[x];
       if (x < warp) {
         base_u += u;
         base_r += sc->warp_rows[x];
+        base_s += g;
       }
       cut.total += u;
-      segs += sc->warp_segs[x];
+      segs += g;
     }
     if (kSnap > 0 && round == 0) {
       const int ctas = list.by_ctas.d;
@@ -259,11 +266,17 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     }
     // threads without the first unit have no more to do (CTA 0's write the items)
     if (round == 1) {
+      if (cut.chunk == 0 && cut.total > static_cast<int>(list.by_ctas.d)) {
+        cut.extra = list.extra;
+        cut.total += list.extra * segs;
+        base_u += list.extra * base_s;
+        units += list.extra * mine_s;
+      }
       if (thread == 0) {
         sc->cut = cut;
         if (blockIdx.x == 0) {
           list.items[n] = cut.total;
-          list.items[n + 1] = cut.chunk;
+          list.items[n + 1] = cut.chunk > 0 ? cut.chunk : -cut.extra;
         }
       }
       const int first = cut.first(blockIdx.x);
@@ -281,7 +294,8 @@ struct PagedWalk {
   int i;
   PagedItem it;
   int ts, rt, first, nt;
-  int item_row, left;
+  int item_row, left, extra;
+  int ntp;        // units of a segment
   int h, ri;      // current piece: KV head, row tile,
   int kt, count;  // first key tile (of the item), tiles
 
@@ -309,16 +323,17 @@ struct PagedWalk {
     it = sc->it;
     item_row = sc->item_row;
     measure();
-    const int off = u0 - sc->item_unit, ntp = cut.padded(nt);
-    const int s = off / ntp;
+    extra = cut.extra;
+    ntp = cut.padded(nt);
+    const int off = u0 - sc->item_unit, s = off / ntp;
     kt = off - s * ntp;
     h = rt == 1 ? s : s / rt;
     ri = s - h * rt;
     count = min(nt - kt, left);
-    return true;
+    return count > 0 || next();  // (the first units may be those behind a segment's tiles)
   }
   __device__ __forceinline__ bool next() {
-    left -= count;
+    left -= ntp - kt;
     if (one || left <= 0) return false;
     kt = 0;
     if (++ri == rt) {
@@ -330,6 +345,7 @@ struct PagedWalk {
           if (++i >= end) return false;
           it = paged_item(*p, i);
           measure();
+          ntp = nt + extra;
         } while (nt == 0);
       }
     }

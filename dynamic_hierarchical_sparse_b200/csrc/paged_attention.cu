@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> int {
     count = 0;
     if (p.nt == 0 || limit <= 0 || !live) return 0;
-    const PagedCut cut{l.items[p.n], l.items[p.n + 1], l.by_ctas};
+    const int how = l.items[p.n + 1];
+    const PagedCut cut{l.items[p.n], max(how, 0), max(-how, 0), l.by_ctas};
     const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt);
     const int row = l.items[p.n + 2 + p.j];
     const int c0 = cut.owner(u0), c1 = cut.owner(u0 + p.nt - 1);
@@ -854,6 +855,13 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
+// Units that a segment counts beside its key tiles, for its Q, its first tile's
+// latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.2 /
+// 61.1 / 60.9 / 61.3 / 61.7, 7 tokens of 16 unshared sequences 42.3 / 38.7 /
+// 34.3 / 34.1 / 33.7, fp32 with 14117 shared and up to 13 own tokens 138 / 77 /
+// 74 / 74 / 76; a list with costly 64-row tiles 27.9 / 29.6 / 30.6 / 32.4 / 33.7.
+constexpr int kSegmentUnits = 2;
+
 // CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
 
@@ -880,6 +888,7 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
+  w.list.extra = kSegmentUnits;
   if (w.prefix.end > 0) {
     w.prefix.by_ctas = FastDiv(sms < kMaxCtas ? sms : kMaxCtas);
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
@@ -901,6 +910,7 @@ cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
+  w.list.extra = kSegmentUnits;
   paged_f32_kernel<D><<<w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -957,7 +967,7 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
                                 : paged_tile_shift<16>(static_cast<int>(r));
     const long long tiles = (r + (1 << ts) - 1) >> ts;
     rows += tiles * p.num_kv_heads << ts;
-    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 1);
+    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 4);
   };
   for (int g = 0; g < G; ++g)
     s.own_prefix ? add(group_rows(g), wide ? 256 : 128, 0, s.prefix_rows)

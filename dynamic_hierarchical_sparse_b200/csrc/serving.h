@@ -74,9 +74,11 @@ cudaError_t launch_kv_append(const PagedArgs& a, int dtype, const dhsa_rope_tabl
 struct PagedList {
   int begin, end;    // items of the list
   FastDiv by_ctas;   // by the CTAs of its grid
+  int extra;         // units of a segment beside its key tiles (see PagedCut)
   float* part_o;     // [rows of all its partials, d]
   float2* part_ml;   // [rows of all its partials]: running max (log2 units), sum
-  int* items;        // [2 (end - begin) + 2]: first key tile of each item, the total, the chunk, first row of each item
+  int* items;        // [2 (end - begin) + 2]: first unit of each item, the total, the chunk
+                     // (or minus the extra units), first row of each item
 };
 
 struct PagedWork {

@@ -26,8 +26,8 @@ def spans(items, hkv, bn, most):
     return out
 
 
-def cut(items, hkv, bn, most, ctas, snap):
-    """(total units, chunk): as paged_schedule decides them; units padded to whole chunks where chunk > 0."""
+def cut(items, hkv, bn, most, ctas, snap, extra):
+    """(total units, chunk, extra units of a segment): as paged_schedule decides them."""
     sp = spans(items, hkv, bn, most)
     total, segs = sum(x[0] for x in sp), sum(hkv * x[3] for x in sp if x[4] > 0)
     chunk = 0
@@ -35,11 +35,14 @@ def cut(items, hkv, bn, most, ctas, snap):
         want = -(-total // (ctas - segs))
         if want <= total // ctas + snap:
             chunk = want
-    return sum(hkv * x[3] * padded(x[4], chunk) for x in sp), chunk
+    if chunk or total <= ctas:
+        extra = 0
+    return sum(hkv * x[3] * padded(x[4], chunk, extra) for x in sp), chunk, extra
 
 
-def padded(nt, chunk):
-    return -(-nt // chunk) * chunk if chunk else nt
+def padded(nt, chunk, extra):
+    """Units of a segment."""
+    return -(-nt // chunk) * chunk if chunk else nt + extra if nt else 0
 
 
 def first(c, total, chunk, ctas):
@@ -53,10 +56,10 @@ def owner(unit, total, chunk, ctas):
     return unit // chunk if chunk else ((unit + 1) * min(ctas, total) - 1) // total
 
 
-def pieces(items, hkv, bn, most, ctas, snap=0):
+def pieces(items, hkv, bn, most, ctas, snap=0, extra=0):
     """Every piece of every CTA: (cta, item, segment, first key tile, tiles, first partial row, rows)."""
     sp = spans(items, hkv, bn, most)
-    total, chunk = cut(items, hkv, bn, most, ctas, snap)
+    total, chunk, extra = cut(items, hkv, bn, most, ctas, snap, extra)
     got = []
     for c in range(ctas):
         u0 = first(c, total, chunk, ctas)
@@ -64,14 +67,15 @@ def pieces(items, hkv, bn, most, ctas, snap=0):
         if left <= 0:
             continue
         unit = row = i = 0
-        units = lambda x: hkv * sp[x][3] * padded(sp[x][4], chunk)  # noqa: E731
+        units = lambda x: hkv * sp[x][3] * padded(sp[x][4], chunk, extra)  # noqa: E731
         while not (units(i) > 0 and unit <= u0 < unit + units(i)):
             unit, row, i = unit + units(i), row + sp[i][1], i + 1
-        seg, kt = divmod(u0 - unit, padded(sp[i][4], chunk))
+        seg, kt = divmod(u0 - unit, padded(sp[i][4], chunk, extra))
         count = min(sp[i][4] - kt, left)
         while True:
-            got.append((c, i, seg, kt, count, c * most + row + seg * sp[i][2], sp[i][2]))
-            left -= count
+            if count > 0:
+                got.append((c, i, seg, kt, count, c * most + row + seg * sp[i][2], sp[i][2]))
+            left -= padded(sp[i][4], chunk, extra) - kt
             if chunk or left <= 0:
                 break
             kt, seg = 0, seg + 1
@@ -81,4 +85,4 @@ def pieces(items, hkv, bn, most, ctas, snap=0):
                 while sp[i][4] == 0:
                     row, i = row + sp[i][1], i + 1
             count = min(sp[i][4], left)
-    return got, sp, total, chunk
+    return got, sp, total, chunk, extra

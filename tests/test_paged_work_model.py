@@ -10,7 +10,7 @@ import pytest
 from tests import paged_work_model as M
 
 
-@pytest.mark.parametrize("seed", range(150))
+@pytest.mark.parametrize("seed", range(250))
 def test_pieces_cover_and_partials_are_apart(seed):
     r = random.Random(seed)
     bn, most = r.choice([(64, 64), (32, 16), (128, 256), (128, 128)])
@@ -19,8 +19,8 @@ def test_pieces_cover_and_partials_are_apart(seed):
     for _ in range(r.randint(1, 30)):
         lo = r.choice([0, 0, r.randint(0, 3000)])
         items.append((r.choice([0, 1, 4, 16, 17, 40, 64, 65, 128, 129, 256, 257, 500]), lo, max(lo, lo + r.randint(-100, 4000))))
-    snap = r.choice([0, 4, 40])
-    got, sp, total, chunk = M.pieces(items, hkv, bn, most, ctas, snap)
+    snap, extra = r.choice([(0, 0), (0, 1), (0, 3), (4, 0), (40, 0)])
+    got, sp, total, chunk, extra = M.pieces(items, hkv, bn, most, ctas, snap, extra)
     rows_total = sum(s[1] for s in sp) + ctas * most
     taken, intervals = {}, []
     for c, i, seg, kt, count, row, rows in got:
@@ -40,13 +40,13 @@ def test_pieces_cover_and_partials_are_apart(seed):
     by = {(c, i, seg): row for c, i, seg, _, _, row, _ in got}
     for i, (units, part, pm, rt, nt) in enumerate(sp):
         for seg in range(hkv * rt if nt else 0):
-            u0 = unit + seg * M.padded(nt, chunk)
+            u0 = unit + seg * M.padded(nt, chunk, extra)
             c0, c1 = M.owner(u0, total, chunk, ctas), M.owner(u0 + nt - 1, total, chunk, ctas)
             first = c0 * most + base + seg * pm
             for c in range(c0, c1 + 1):
                 assert by[c, i, seg] == first + (c - c0) * most
                 assert any(taken[i, seg, x] == c for x in range(nt))
-        unit, base = unit + hkv * rt * M.padded(nt, chunk), base + part
+        unit, base = unit + hkv * rt * M.padded(nt, chunk, extra), base + part
 
 
 def test_division_by_a_product():
