@@ -726,6 +726,9 @@ class KvAppender:
             hq = q.shape[1]
             if q_out is None:
                 q_out = torch.empty(T, hq, d, dtype=dt, device=c.device)
+                if stream is not None:  # memory of the current stream, written on another
+                    stream.wait_stream(torch.cuda.current_stream(c.device))
+                    q_out.record_stream(stream)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if positions is not None:

@@ -80,6 +80,8 @@ class Step:
             lo = 0 if first_of[b] == b else prefix_of[b]
             for i in range(lo // page, -(-cover[b] // page)):
                 a, e = max(lo, i * page), min(cover[b], (i + 1) * page)
+                if e <= a:  # the sequence ends within the prefix
+                    continue
                 k = torch.randn(hkv, e - a, d, generator=g)
                 if values == "peaks":
                     k += 0.5 * torch.randn(hkv, e - a, 4, generator=g) @ mix
