@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "launch_early.cuh"
 #include "serving.h"
 
 namespace dhsa {
@@ -23,15 +24,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-// Programmatic dependent launch: a call's later kernels are launched while the
-// earlier ones run.  `let_next_start` is given by every CTA of a kernel (or by
-// its exit); `wait_for_previous` returns when the kernel before has completed
-// and its writes are visible.  The prefixes' kernel and the list's kernel read
-// the call's inputs only, so the second need not wait for the first to begin,
-// but it waits before it ends: its completion then stands for both.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // One item: the query tokens [t0, t1) over the keys [lo, hi) of a table row.
 struct PagedItem {

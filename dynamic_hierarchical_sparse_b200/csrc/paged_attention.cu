@@ -447,6 +447,10 @@ __device__ __forceinline__ bool open_list(const PagedWork& w, unsigned char* sme
     *ctx.abort_flag = 0;
     fence_mbar_init();
   }
+  // The prefixes' kernel before this one, if any, has waited for what the call
+  // reads, and writes nothing that this kernel reads or writes: no need to wait
+  // for its end before this kernel's own (whose completion then stands for both).
+  if (w.prefix.end == 0) wait_for_previous();
   paged_schedule<BN, kMax, kMmaThreads, 0>(w.p, w.by_group.d, w.list, sc, w.status);
   __syncthreads();
   let_next_start();
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
       }
     } while (ok && walk.next());
   }
-  wait_for_previous();  // of the prefixes' kernel, see paged.cuh
+  wait_for_previous();  // the prefixes' kernel, see open_list
 }
 
 // ------------------------------------------------------------------ fp32
@@ -710,6 +714,7 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
 // after its end with 4, 6.0 with 1; 128 rows: 2.8 with 4, 3.6 with 1).
 template <int D, typename T, int BN, int kMax, int WARPS>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
+  let_next_start();
   constexpr int kCols = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x, h = blockIdx.y * (4 / WARPS) + warp / WARPS;
@@ -838,23 +843,6 @@ int sm_count() {
   return sms;
 }
 
-// `early`: launched while the kernel before it in the stream still runs.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, bool early,
-                         const A&... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid;
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = attr;
-  c.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
 // Units that a segment counts beside its key tiles, for its Q, its first tile's
 // latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.2 /
 // 61.1 / 60.9 / 61.3 / 61.7, 7 tokens of 16 unshared sequences 42.3 / 38.7 /
@@ -871,9 +859,9 @@ template <int D, typename T, int BN, int kMax>
 cudaError_t join(const PagedWork& w, cudaStream_t stream) {
   const long long rows = static_cast<long long>(w.p.total_q) * w.num_q_heads;
   if (rows <= kFewRows)
-    return launch_after(paged_join_kernel<D, T, BN, kMax, 4>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, true, w);
-  return launch_after(paged_join_kernel<D, T, BN, kMax, 1>, dim3(w.p.total_q, (w.num_q_heads + 3) / 4), 128, 0, stream,
-                      true, w);
+    return launch_early(paged_join_kernel<D, T, BN, kMax, 4>, dim3(w.p.total_q, w.num_q_heads), 128, 0, stream, w);
+  return launch_early(paged_join_kernel<D, T, BN, kMax, 1>, dim3(w.p.total_q, (w.num_q_heads + 3) / 4), 128, 0, stream,
+                      w);
 }
 
 template <int D, int kMax>
@@ -893,7 +881,7 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
     w.prefix.by_ctas = FastDiv(sms < kMaxCtas ? sms : kMaxCtas);
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
   }
-  e = launch_after(paged_mma_kernel<D, kMax>, w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream, w.prefix.end > 0, mk, mv, w);
+  e = launch_early(paged_mma_kernel<D, kMax>, w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream, mk, mv, w);
   if (e != cudaSuccess) return e;
   return join<D, __nv_bfloat16, kBN, kMax>(w, stream);
 }
@@ -911,8 +899,7 @@ cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
   w.list.extra = kSegmentUnits;
-  paged_f32_kernel<D><<<w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream>>>(mk, mv, w);
-  e = cudaGetLastError();
+  e = launch_early(paged_f32_kernel<D>, w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream, mk, mv, w);
   if (e != cudaSuccess) return e;
   return join<D, float, kFBN, kFRows>(w, stream);
 }

@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     // 8 warps x 224 + 4 x 56 registers = the launch's 12 x 168
     if constexpr (C::kLanes == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // this warpgroup lays out the CTA's work while the softmax warps warm up
+    wait_for_previous();
     paged_schedule<kBN, C::kRows, 128, kSnapTiles>(w.p, gh, w.prefix, sc, w.status);
     let_next_start();
     __syncthreads();
@@ -517,6 +518,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       if (!ok) break;
       if (rehearsal) {
         rehearsal = false;
+        wait_for_previous();
         __syncthreads();  // the schedule is there; what this round wrote to TMEM is behind tc_fence_before
         if (!walk.init(&w.p, gh, w.prefix, sc)) break;
         send_q(walk);
@@ -623,8 +625,7 @@ cudaError_t run(const PagedWork& w, cudaStream_t stream) {
   cudaError_t e =
       cudaFuncSetAttribute(paged_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  paged_prefix_kernel<D><<<w.prefix.by_ctas.d, C::kThreads, C::kSmemBytes, stream>>>(mk, mv, w);
-  return cudaGetLastError();
+  return launch_early(paged_prefix_kernel<D>, w.prefix.by_ctas.d, C::kThreads, C::kSmemBytes, stream, mk, mv, w);
 }
 
 }  // namespace

@@ -27,6 +27,7 @@
 // and reading the table by generic address instead of through the constant
 // bank (one lane at a time) another 10 to 20 % at 2 and 4.
 #include "common.cuh"
+#include "launch_early.cuh"
 #include "serving.h"
 
 namespace dhsa {
@@ -155,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     rope_kernel(const __grid_constant__ dhsa_rope_table rope, const __grid_constant__ RopeArgs a) {
   using C = RopeCfg<T, D, VEC, HEADS, PAGED>;
   using V = Vec<T, VEC>;
+  let_next_start();
+  wait_for_previous();
   const int cq = (a.q.heads + C::kChunk - 1) / C::kChunk, ck = (a.k.heads + C::kChunk - 1) / C::kChunk;
   const int cv = PAGED ? (a.v.heads + C::kChunk - 1) / C::kChunk : 0;
   const unsigned chunks = cq + ck + cv;
@@ -326,8 +329,7 @@ cudaError_t run(const dhsa_rope_table& rope, const RopeArgs& a, cudaStream_t str
                            (PAGED ? (a.v.heads + C::kChunk - 1) / C::kChunk : 0);
   const long long blocks = (a.tokens * chunks + C::kUnits - 1) / C::kUnits;
   if (blocks * C::kUnits > INT32_MAX) return cudaErrorInvalidValue;
-  rope_kernel<T, D, VEC, HEADS, PAGED><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(rope, a);
-  return cudaGetLastError();
+  return launch_early(rope_kernel<T, D, VEC, HEADS, PAGED>, static_cast<unsigned>(blocks), kThreads, 0, stream, rope, a);
 }
 
 // W: numbers of a 16-byte vector.
