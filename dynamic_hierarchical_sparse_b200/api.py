@@ -536,7 +536,7 @@ def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dty
         n, h, d = t.shape
         st, sh, sd = t.stride()
         if (h == heads and d == head_dim and n >= tokens and sd == 1 and (sh == d or h == 1) and t.dtype is dtype
-                and t.get_device() == index):
+                and t.get_device() == index and (st >= h * d or n <= 1)):
             return _Tokens(t.data_ptr(), st if n > 1 else h * d)
     # what of it is wrong
     if t.get_device() != index:
@@ -545,7 +545,9 @@ def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dty
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.ndim != 3 or n < tokens or h != heads or d != head_dim:
         raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(t.shape)))
-    raise ValueError("the heads of a token of %s must be contiguous" % name)
+    if sd != 1 or (sh != d and h > 1):
+        raise ValueError("the heads of a token of %s must be contiguous" % name)
+    raise ValueError("the tokens of %s overlap (a broadcast tensor must be expanded to memory of its own)" % name)
 
 
 def _int32(t: torch.Tensor, name: str, shape, index: int) -> None:

@@ -17,10 +17,16 @@
 // tile's keys (each with its own running max and O, joined when the piece
 // ends), with 32 two split them, with 64 every warp has 16 rows of its own.
 // Q stays in registers, P goes from the S fragments straight into the A
-// operand of P V (f16, as V).
+// operand of P V (f16, as V).  Measured: 48 unshared sequences of 100 to 8192
+// keys, 32 + 8 heads of 128: 135 us for 839 MB, 6.2 TB/s (0.95 of the measured copy
+// rate), of which the join has 4.  A short call (4 sequences, 128 rows, 10.3 us)
+// is latency: the first pass over the code, one round of loads, the join.
 //
 // paged_f32_kernel (fp32): the same with 32-key tiles and 16 rows, on tf32
-// fragments in pairs.
+// fragments in pairs.  Bound by its products: an m16n8k8 takes 8 cycles of a
+// quarter of an SM whatever of its 16 rows is in use, and a product is three of
+// them.  Measured: 4 sequences on 14117 keys, 32 + 8 heads: 75 us with d 256, 42
+// with d 128 (231 and 116 MB).
 #include "launchers.h"
 #include "paged.cuh"
 
@@ -32,11 +38,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The prefixes are a list of their own, for the tcgen05 kernel, where a group
 // has more than 32 rows (query tokens times Hq / Hkv) and the prefixes may be
 // long: rows x Hkv x d x the tokens that a table row has room for (their lengths
-// are on the device) of 2^30 or more.  That kernel costs about 10 us more to
-// start and end; 32 + 8 heads of 128, page 16, one kernel / two, in us: 16
-// sequences on 1024 keys 21.9 / 27.9, on 8192 30.9 / 36.7, 32 on 2048 28.4 /
-// 37.5, 12 on 32768 58.0 / 53.7, 32 on 32768 106 / 71; 64 of d 64 on 1024
-// 27.0 / 35.7; 24 sequences of 5 tokens, 8 + 4 heads of 256, on 4097 62 / 50.
+// are on the device) of 2^30 or more.  That kernel costs a few us more to start
+// and end; 32 + 8 heads of 128, page 16, up to 512 own keys, one kernel / two, in
+// us: 16 sequences on 1024 keys 20.9 / 23.1, on 8192 32.2 / 32.0, 32 on 2048
+// 32.3 / 32.2, 12 on 32768 57.1 / 50.0, 32 on 32768 104 / 60, 64 on 131072 575 /
+// 187; 64 of d 64 on 1024 26.8 / 29.8; 12 sequences of 5 tokens in two groups,
+// 8 + 4 heads of 256, on 4097 65.5 / 41.3.
 constexpr int kOwnPrefixRows = 32;
 constexpr long long kOwnPrefixWork = 1ll << 30;
 
@@ -710,8 +717,9 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
 // each a share of its partials, and join in the order of the warps: 4 where the
 // rows are few, so that a row's partials are all in flight at once, and 1 where they
 // are many, so that the CTAs are few enough to be there, their places
-// looked up, when the kernel before ends (2048 rows of 19 partials: 10.0 us
-// after its end with 4, 6.0 with 1; 128 rows: 2.8 with 4, 3.6 with 1).
+// looked up, when the kernel before ends.  The whole call with 4 / 1, in us: 128
+// rows 10.3 / 11.4, 1024 rows 59.9 / 62.5, 1536 rows 135.9 / 134.3, 2048 rows
+// 188.1 / 187.6.
 template <int D, typename T, int BN, int kMax, int WARPS>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
   let_next_start();
@@ -844,10 +852,12 @@ int sm_count() {
 }
 
 // Units that a segment counts beside its key tiles, for its Q, its first tile's
-// latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.2 /
-// 61.1 / 60.9 / 61.3 / 61.7, 7 tokens of 16 unshared sequences 42.3 / 38.7 /
-// 34.3 / 34.1 / 33.7, fp32 with 14117 shared and up to 13 own tokens 138 / 77 /
-// 74 / 74 / 76; a list with costly 64-row tiles 27.9 / 29.6 / 30.6 / 32.4 / 33.7.
+// latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.0 /
+// 60.2 / 59.8 / 60.5 / 60.8, 7 tokens of 16 unshared sequences 38.3 / 28.2 /
+// 26.5 / 26.0 / 27.0, 5 tokens on 4097 keys, d 256, 47.0 / 43.4 / 41.5 / 42.3 /
+// 43.0, fp32 with 14117 shared and up to 13 own tokens 138 / 78 / 75 / 74 / 76; a
+// list with costly 64-row tiles (16 answers to 8192 tokens, where a tile takes
+// 2.6 times a 16-row one) 30.4 / 31.6 / 32.4 / 32.1 / 34.3.
 constexpr int kSegmentUnits = 2;
 
 // CTAs of a grid at most: what the partials are sized for.

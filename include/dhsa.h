@@ -507,7 +507,9 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * below a sequence's kv_lens, or in a shared prefix, may reach all the query
  * rows that are worked on together, also those to which the position is not
  * visible; keys (K), and slots at or behind kv_lens, reach no row that does not
- * see them.  Results are the same from call to call.  A batch whose tables
+ * see them.  An infinity in a query or a visible key of an fp32 problem makes
+ * the row NaN (its products are taken in two parts, see paged_attention.cu); in
+ * bf16 it is an infinite score, as in plain arithmetic.  Results are the same from call to call.  A batch whose tables
  * leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
  * 32 keys is refused as DHSA_ERR_UNSUPPORTED.
  *   q, out     [T, Hq, d] in the cache's dtype; must not overlap

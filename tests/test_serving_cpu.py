@@ -311,3 +311,22 @@ def test_struct_layouts_match_the_header():
                        check=True)
         got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == [ctypes.sizeof(c) for c in names.values()]
+
+
+# ------------------------------------------------------------ operands of the binding
+
+
+def test_broadcast_tokens_are_refused():
+    """A tensor whose tokens share memory has the stride that would stand for packed tokens."""
+    x = torch.zeros(1, 4, 64, dtype=torch.bfloat16).expand(3, 4, 64)
+    with pytest.raises(ValueError, match="q overlap"):
+        api._tokens(x, "q", 4, 64, torch.bfloat16, 3, x.get_device())
+    half = torch.zeros(4 * 256, dtype=torch.bfloat16).as_strided((3, 4, 64), (128, 64, 1))
+    with pytest.raises(ValueError, match="q overlap"):
+        api._tokens(half, "q", 4, 64, torch.bfloat16, 3, half.get_device())
+    with pytest.raises(ValueError, match="contiguous"):
+        api._tokens(torch.zeros(3, 4, 128, dtype=torch.bfloat16)[:, :, ::2], "q", 4, 64, torch.bfloat16, 3, -1)
+    one = torch.zeros(1, 4, 64, dtype=torch.bfloat16).expand(1, 4, 64)
+    assert api._tokens(one, "q", 4, 64, torch.bfloat16, 1, -1).token_stride == 4 * 64
+    apart = torch.zeros(3, 4, 128, dtype=torch.bfloat16)[:, :2].reshape(3, 4, 64)
+    assert api._tokens(apart[:, :2], "q", 2, 64, torch.bfloat16, 3, -1).token_stride == 4 * 128
