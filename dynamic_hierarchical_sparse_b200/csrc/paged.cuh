@@ -93,6 +93,16 @@ __host__ __device__ __forceinline__ int paged_tile_shift(int rows) {
   return m;
 }
 
+// Units that a key tile counts, by log2 of its rows (see PagedCut): in the kernel
+// with tiles of up to 64 rows one of 64 takes about 2.6 times as long as one of
+// 16.  Counting every tile alike / 1, 2, 3, in us (32 + 8 heads of 128, up to 512
+// own keys): 16 sequences on 1024 shared keys 21.0 / 17.6, on 8192 32.1 / 29.4, 32
+// on 2048 32.1 / 24.0; of d 256, 16 on 1000 45.0 / 29.9.
+template <int kMax>
+__host__ __device__ __forceinline__ constexpr int paged_tile_units(int ts) {
+  return kMax != 64 ? 1 : ts - 3;
+}
+
 // An item's segments and key tiles.
 template <int BN, int kMaxRows>
 struct PagedSpan {
@@ -108,19 +118,25 @@ struct PagedSpan {
   }
 };
 
-// How a list's units (fewer than 2^30) are cut among the CTAs.  chunk 0: a
-// segment counts its key tiles and `extra` units behind them, for what its
-// start and end cost (none where there are no more tiles than CTAs), and the
-// units are cut evenly, wherever that falls; with fewer units than CTAs the
-// first `total` CTAs take one each, so every CTA between the owners of a
+// How a list's units (fewer than 2^30) are cut among the CTAs.  chunk 0: the
+// units are cut evenly, wherever that falls, and a key tile belongs to the CTA
+// that holds its first unit.  extra > 0: a tile counts paged_tile_units, and a
+// segment the units of `extra` more tiles behind its own, for what its start and
+// end cost; every CTA has at least as many units as any tile counts.  extra 0
+// (short lists): a tile is one unit, and with fewer units than CTAs the first
+// `total` CTAs take one each.  Either way every CTA between the owners of a
 // segment's first and last tile has a partial of it.
 // chunk > 0: every segment counts as a whole number of chunks, a CTA takes one
 // chunk, and none has two segments.
 struct PagedCut {
   int total, chunk, extra;
   FastDiv by_ctas;
-  __device__ __forceinline__ int padded(int nt) const {  // a segment's units
-    return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt > 0 ? nt + extra : 0;
+  template <int kMax>
+  __device__ __forceinline__ int tile_units(int ts) const {
+    return extra > 0 ? paged_tile_units<kMax>(ts) : 1;
+  }
+  __device__ __forceinline__ int padded(int nt, int wt) const {  // a segment's units
+    return chunk > 0 ? (nt + chunk - 1) / chunk * chunk : nt > 0 ? (nt + extra) * wt : 0;
   }
   __device__ __forceinline__ int first(int c) const {  // the first unit of CTA c: c * total / ctas
     if (chunk > 0) return min(c * chunk, total);
@@ -187,7 +203,7 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
       const PagedItem it = paged_item(p, list.begin + i);
       const PagedSpan<BN, kMaxRows> sp(it, group_heads);
       const int tiles = p.num_kv_heads * sp.rt;
-      const int du = tiles * cut.padded(sp.nt);
+      const int du = tiles * cut.padded(sp.nt, cut.tile_units<kMaxRows>(sp.ts));
       const int dr = tiles << sp.ts;
       if (find) {
         if (du > 0 && units <= mine && mine < units + du) {
@@ -210,7 +226,10 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
       }
       units += du;
       rows += dr;
-      segs += sp.nt > 0 ? tiles : 0;
+      // segments, or (no chunks) the units that they count beside their tiles
+      segs += sp.nt == 0 ? 0
+              : kSnap > 0 ? tiles
+                          : tiles * ((sp.nt + list.extra) * paged_tile_units<kMaxRows>(sp.ts) - sp.nt);
     }
     if (find) break;
     if (bad) report(status, kDevCheck);
@@ -258,11 +277,12 @@ __device__ __forceinline__ void paged_schedule(const PagedArgs& p, int group_hea
     }
     // threads without the first unit have no more to do (CTA 0's write the items)
     if (round == 1) {
-      if (cut.chunk == 0 && cut.total > static_cast<int>(list.by_ctas.d)) {
+      const int ctas = list.by_ctas.d;
+      if (kSnap == 0 && cut.total > ctas && cut.total + segs >= paged_tile_units<kMaxRows>(6) * ctas) {
         cut.extra = list.extra;
-        cut.total += list.extra * segs;
-        base_u += list.extra * base_s;
-        units += list.extra * mine_s;
+        cut.total += segs;
+        base_u += base_s;
+        units += mine_s;
       }
       if (thread == 0) {
         sc->cut = cut;
@@ -287,7 +307,8 @@ struct PagedWalk {
   PagedItem it;
   int ts, rt, first, nt;
   int item_row, left, extra;
-  int ntp;        // units of a segment
+  int wt, ntp;    // units of a key tile, of a segment
+  int skip;       // units of the segment before this CTA's
   int h, ri;      // current piece: KV head, row tile,
   int kt, count;  // first key tile (of the item), tiles
 
@@ -316,18 +337,25 @@ struct PagedWalk {
     item_row = sc->item_row;
     measure();
     extra = cut.extra;
-    ntp = cut.padded(nt);
+    wt = cut.tile_units<kMaxRows>(ts);
+    ntp = cut.padded(nt, wt);
     const int off = u0 - sc->item_unit, s = off / ntp;
-    kt = off - s * ntp;
+    skip = off - s * ntp;
     h = rt == 1 ? s : s / rt;
     ri = s - h * rt;
-    count = min(nt - kt, left);
+    kt = tiles(skip);
+    count = min(nt, tiles(skip + left)) - kt;
     return count > 0 || next();  // (the first units may be those behind a segment's tiles)
   }
+  // key tiles whose first unit is among the segment's first n
+  __device__ __forceinline__ int tiles(int n) const {
+    return kMaxRows == 64 ? (n + wt - 1) / wt : n;
+  }
   __device__ __forceinline__ bool next() {
-    left -= ntp - kt;
+    left -= ntp - skip;
     if (one || left <= 0) return false;
     kt = 0;
+    skip = 0;
     if (++ri == rt) {
       ri = 0;
       if (++h == p->num_kv_heads) {
@@ -337,11 +365,12 @@ struct PagedWalk {
           if (++i >= end) return false;
           it = paged_item(*p, i);
           measure();
-          ntp = nt + extra;
+          if (kMaxRows == 64 && extra > 0) wt = paged_tile_units<kMaxRows>(ts);
+          ntp = (nt + extra) * wt;
         } while (nt == 0);
       }
     }
-    count = min(nt, left);
+    count = min(nt, tiles(left));
     return true;
   }
 };

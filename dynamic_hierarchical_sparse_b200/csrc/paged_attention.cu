@@ -40,10 +40,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // long: rows x Hkv x d x the tokens that a table row has room for (their lengths
 // are on the device) of 2^30 or more.  That kernel costs a few us more to start
 // and end; 32 + 8 heads of 128, page 16, up to 512 own keys, one kernel / two, in
-// us: 16 sequences on 1024 keys 20.9 / 23.1, on 8192 32.2 / 32.0, 32 on 2048
-// 32.3 / 32.2, 12 on 32768 57.1 / 50.0, 32 on 32768 104 / 60, 64 on 131072 575 /
-// 187; 64 of d 64 on 1024 26.8 / 29.8; 12 sequences of 5 tokens in two groups,
-// 8 + 4 heads of 256, on 4097 65.5 / 41.3.
+// us: 16 sequences on 1024 keys 17.4 / 24.1, on 16384 38.7 / 38.4, 32 on 2048
+// 24.2 / 32.5, on 8192 39.1 / 37.5, 12 on 32768 56.5 / 49.9, 32 on 32768 103 /
+// 60, 64 on 131072 591 / 189; 64 of d 64 on 1024 24.7 / 29.6, 16 of d 256 on 2000
+// 31.0 / 35.2, on 8000 52.4 / 47.7; 12 sequences of 5 tokens in two groups, 8 + 4
+// heads of 256, on 4097 52.0 / 43.0.
 constexpr int kOwnPrefixRows = 32;
 constexpr long long kOwnPrefixWork = 1ll << 30;
 
@@ -756,9 +757,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     if (p.nt == 0 || limit <= 0 || !live) return 0;
     const int how = l.items[p.n + 1];
     const PagedCut cut{l.items[p.n], max(how, 0), max(-how, 0), l.by_ctas};
-    const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt);
+    // (the prefixes' own list has no extra tiles: there a tile is one)
+    const int wt = cut.tile_units<kMax>(p.ts);
+    const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt, wt);
     const int row = l.items[p.n + 2 + p.j];
-    const int c0 = cut.owner(u0), c1 = cut.owner(u0 + p.nt - 1);
+    const int c0 = cut.owner(u0), c1 = cut.owner(u0 + (p.nt - 1) * wt);
     count = c1 - c0 + 1;
     return paged_part_row(c0, step, row, p.seg, p.ts) + p.in_tile;
   };
@@ -851,14 +854,13 @@ int sm_count() {
   return sms;
 }
 
-// Units that a segment counts beside its key tiles, for its Q, its first tile's
+// Key tiles that a segment counts beside its own, for its Q, its first tile's
 // latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.0 /
-// 60.2 / 59.8 / 60.5 / 60.8, 7 tokens of 16 unshared sequences 38.3 / 28.2 /
-// 26.5 / 26.0 / 27.0, 5 tokens on 4097 keys, d 256, 47.0 / 43.4 / 41.5 / 42.3 /
-// 43.0, fp32 with 14117 shared and up to 13 own tokens 138 / 78 / 75 / 74 / 76; a
-// list with costly 64-row tiles (16 answers to 8192 tokens, where a tile takes
-// 2.6 times a 16-row one) 30.4 / 31.6 / 32.4 / 32.1 / 34.3.
-constexpr int kSegmentUnits = 2;
+// 60.2 / 59.8 / 60.5 / 60.8, 5 tokens on 4097 keys, d 256, 47.0 / 43.4 / 41.5 /
+// 42.3 / 43.0, fp32 with 14117 shared and up to 13 own tokens 138 / 78 / 75 / 74
+// / 76; with 1 / 2 / 3: 7 tokens of 16 unshared sequences 28.6 / 26.7 / 25.8, 16
+// answers to 8192 tokens 31.1 / 29.4 / 28.7, 32 to 2048 25.7 / 24.0 / 25.7.
+constexpr int kSegmentTiles = 2;
 
 // CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
@@ -886,7 +888,7 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
-  w.list.extra = kSegmentUnits;
+  w.list.extra = kSegmentTiles;
   if (w.prefix.end > 0) {
     w.prefix.by_ctas = FastDiv(sms < kMaxCtas ? sms : kMaxCtas);
     if ((e = launch_paged_prefix(w, stream)) != cudaSuccess) return e;
@@ -908,7 +910,7 @@ cudaError_t run_f32(PagedWork w, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.list.by_ctas = FastDiv(sms * C::kCtas < kMaxCtas ? sms * C::kCtas : kMaxCtas);
-  w.list.extra = kSegmentUnits;
+  w.list.extra = kSegmentTiles;
   e = launch_early(paged_f32_kernel<D>, w.list.by_ctas.d, kMmaThreads, C::kSmemBytes, stream, mk, mv, w);
   if (e != cudaSuccess) return e;
   return join<D, float, kFBN, kFRows>(w, stream);
@@ -964,7 +966,8 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
                                 : paged_tile_shift<16>(static_cast<int>(r));
     const long long tiles = (r + (1 << ts) - 1) >> ts;
     rows += tiles * p.num_kv_heads << ts;
-    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 4);
+    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 4) *
+                (max == 64 ? paged_tile_units<64>(ts) : 1);
   };
   for (int g = 0; g < G; ++g)
     s.own_prefix ? add(group_rows(g), wide ? 256 : 128, 0, s.prefix_rows)

@@ -67,18 +67,18 @@ cudaError_t launch_kv_append(const PagedArgs& a, int dtype, const dhsa_rope_tabl
 // tokens that walk one range of keys: the groups' shared prefixes first, then
 // every sequence's own part.  An item has Hkv * ceil(rows / its tile's rows)
 // segments (rows = its tokens times Hq / Hkv), each of all its key tiles; the
-// key tiles of all segments, in order, are cut evenly among the CTAs, and a CTA
-// leaves one partial result (O unnormalised, running max, sum) for each segment
+// key tiles of all segments, in order, are cut among the CTAs, by what they cost,
+// and a CTA leaves one partial result (O unnormalised, running max, sum) for each segment
 // that it touches.  One kernel works on one list: all items, or the prefixes
 // and the sequences in a list each.
 struct PagedList {
   int begin, end;    // items of the list
   FastDiv by_ctas;   // by the CTAs of its grid
-  int extra;         // units of a segment beside its key tiles (see PagedCut)
+  int extra;         // key tiles that a segment counts beside its own (see PagedCut)
   float* part_o;     // [rows of all its partials, d]
   float2* part_ml;   // [rows of all its partials]: running max (log2 units), sum
   int* items;        // [2 (end - begin) + 2]: first unit of each item, the total, the chunk
-                     // (or minus the extra units), first row of each item
+                     // (or minus the extra tiles), first row of each item
 };
 
 struct PagedWork {

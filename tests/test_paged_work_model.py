@@ -38,15 +38,17 @@ def test_pieces_cover_and_partials_are_apart(seed):
     # the join's view
     unit = base = 0
     by = {(c, i, seg): row for c, i, seg, _, _, row, _ in got}
-    for i, (units, part, pm, rt, nt) in enumerate(sp):
+    for i, (_, part, pm, rt, nt) in enumerate(sp):
+        units = M.padded(sp[i], most, chunk, extra)
         for seg in range(hkv * rt if nt else 0):
-            u0 = unit + seg * M.padded(nt, chunk, extra)
-            c0, c1 = M.owner(u0, total, chunk, ctas), M.owner(u0 + nt - 1, total, chunk, ctas)
+            u0 = unit + seg * units
+            last = u0 + (nt - 1) * M.weight(sp[i], most, extra)
+            c0, c1 = M.owner(u0, total, chunk, ctas), M.owner(last, total, chunk, ctas)
             first = c0 * most + base + seg * pm
             for c in range(c0, c1 + 1):
                 assert by[c, i, seg] == first + (c - c0) * most
                 assert any(taken[i, seg, x] == c for x in range(nt))
-        unit, base = unit + hkv * rt * M.padded(nt, chunk, extra), base + part
+        unit, base = unit + hkv * rt * units, base + part
 
 
 def test_division_by_a_product():
