@@ -42,9 +42,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // and end; 32 + 8 heads of 128, page 16, up to 512 own keys, one kernel / two, in
 // us: 16 sequences on 1024 keys 17.4 / 24.1, on 16384 38.7 / 38.4, 32 on 2048
 // 24.2 / 32.5, on 8192 39.1 / 37.5, 12 on 32768 56.5 / 49.9, 32 on 32768 103 /
-// 60, 64 on 131072 591 / 189; 64 of d 64 on 1024 24.7 / 29.6, 16 of d 256 on 2000
-// 31.0 / 35.2, on 8000 52.4 / 47.7; 12 sequences of 5 tokens in two groups, 8 + 4
-// heads of 256, on 4097 52.0 / 43.0.
+// 60, 64 on 131072 591 / 189; 64 of d 64 on 1024 24.7 / 29.6, 16 of d 256 on
+// 8000 52.4 / 42.0; 12 sequences of 5 tokens in two groups, 8 + 4 heads of 256,
+// on 4097 52.0 / 39.2.
 constexpr int kOwnPrefixRows = 32;
 constexpr long long kOwnPrefixWork = 1ll << 30;
 
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   Place pp{0, 0, 0, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
-    pp = own_list ? place(PagedSpan<kPrefixBN, kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
+    pp = own_list ? place(PagedSpan<paged_prefix_keys(D), kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
   }
   const Place po = place(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
   wait_for_previous();
@@ -966,7 +966,7 @@ PagedShape paged_shape(const PagedArgs& p, const int* h_cu_q, const int* h_group
                                 : paged_tile_shift<16>(static_cast<int>(r));
     const long long tiles = (r + (1 << ts) - 1) >> ts;
     rows += tiles * p.num_kv_heads << ts;
-    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? kPrefixBN : bf16 ? kBN : kFBN) + 4) *
+    units[x] += tiles * p.num_kv_heads * (cap / (x == 0 ? paged_prefix_keys(p.head_dim) : bf16 ? kBN : kFBN) + 4) *
                 (max == 64 ? paged_tile_units<64>(ts) : 1);
   };
   for (int g = 0; g < G; ++g)

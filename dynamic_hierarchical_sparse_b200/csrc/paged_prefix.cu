@@ -17,7 +17,10 @@
 // the same rows and take every other key tile, and join when the piece ends.  K and V
 // tiles come into rings of 2 and 3 (4 and 4 for d 64).  P is handed over in two
 // halves of 64 keys, so the first half's products run beside the second half's
-// exponentials.  d 256 has TMEM and shared memory for one lane.
+// exponentials.  d 256 has TMEM and shared memory for one lane, with key tiles of
+// 64 in the same rings: S of the next tile then runs beside this tile's softmax, and
+// loads are in flight all the time (32 answers to 32000 tokens: a call of 82 us
+// against 106 with key tiles of 128 in rings of one).
 //
 // The two issuing threads take turns, a tile's P V and the next S to a turn:
 // with MMAs of both lanes mixed, one by one, a call of 64 answers to 128K tokens
@@ -40,7 +43,6 @@ namespace dhsa {
 namespace {
 
 constexpr int kBM = 128;  // rows of a lane's tile
-constexpr int kBN = kPrefixBN;
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last
 // time: weights then reach 256 instead of 1, which f16 holds with the same
 // relative rounding (2^-11), and most tiles skip the pass over O.
@@ -99,27 +101,30 @@ constexpr int kSnapTiles = 4;
 
 template <int D>
 struct PrefixCfg {
+  static constexpr int kBN = paged_prefix_keys(D);
   static constexpr int kLanes = D == 256 ? 1 : 2;
   static constexpr int kRows = paged_prefix_rows(D);  // of a row tile
   static constexpr int kThreads = 128 * (kLanes + 1);
   static constexpr int kProducer = 4 * kLanes;
   static constexpr int kMma = kProducer + 1;  // + lane
   static constexpr int kProducerV = kProducer + 3;
-  static constexpr int kKStages = D == 256 ? 1 : D == 128 ? 2 : 4;
-  static constexpr int kVStages = D == 256 ? 1 : D == 128 ? 3 : 4;
+  static constexpr int kKStages = D == 64 ? 4 : 2;
+  static constexpr int kVStages = D == 64 ? 4 : 3;
   static constexpr int kSlices = D / 64;
   static constexpr int kSub = kBN * 128;  // one 64-column slice of a tile
   static constexpr int kTile = kSlices * kSub;
+  static constexpr int kSubQ = kBM * 128;
+  static constexpr int kTileQ = kSlices * kSubQ;
   static constexpr int kOffQ = 0;  // + lane
-  static constexpr int kOffK = kLanes * kTile;
+  static constexpr int kOffK = kLanes * kTileQ;
   static constexpr int kOffV = kOffK + kKStages * kTile;
   static constexpr int kOffScan = kOffV + kVStages * kTile;
   static constexpr int kOffBar = kOffScan + ((static_cast<int>(sizeof(PagedScan)) + 15) / 16) * 16;
   static constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kColS = 0;              // + 128 * lane
-  static constexpr uint32_t kColO = 128 * kLanes;   // + D * lane
-  static_assert(kLanes * (128 + D) <= 512, "TMEM budget");
+  static constexpr uint32_t kColS = 0;         // + kBN * (lane, or the tile's parity with one lane)
+  static constexpr uint32_t kColO = 2 * kBN;   // + D * lane
+  static_assert(2 * kBN + kLanes * D <= 512, "TMEM budget");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     paged_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedWork w) {
   using C = PrefixCfg<D>;
+  constexpr int kBN = C::kBN;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -173,6 +179,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   // Two lanes on one set of rows take every other key tile of a piece
   // (`apart`): lane a's tiles are a, a + 2, ...; otherwise every one.
   auto apart = [&]() -> bool { return C::kLanes == 2 && walk.ts < 8; };
+  // The S and P of a lane's tile n, counted across pieces: two lanes have a place
+  // and barriers each, one lane takes two by turns (S of the next tile is done
+  // before P V of this one is sent, and neither side gets two tiles ahead on one).
+  auto p_bar = [](int a, int n) { return C::kLanes == 2 ? a : n & 1; };
+  auto p_phase = [](int n) { return static_cast<uint32_t>((C::kLanes == 2 ? n : n >> 1) & 1); };
 
   if (warp >= C::kProducer) {
     // 8 warps x 224 + 4 x 56 registers = the launch's 12 x 168
@@ -238,8 +249,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int a = warp - C::kMma;
         constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, 0);
         constexpr uint32_t idesc_o = idesc_f16_f32(kBM, D, 1);  // P and V in f16
-        const uint32_t tS = tmem + C::kColS + 128 * a, tO = tmem + C::kColO + D * a;
-        const uint32_t qbase = sbase + C::kOffQ + a * C::kTile;
+        const uint32_t tS0 = tmem + C::kColS, tO = tmem + C::kColO + D * a;
+        const uint32_t qbase = sbase + C::kOffQ + a * C::kTileQ;
         // turn x (counted across pieces): lane 1 waits for lane 0's turn x, lane 0 for lane 1's turn x - 1
         auto wait_turn = [&](int x) -> bool {
           if (C::kLanes == 1) return true;
@@ -269,40 +280,59 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             const bool pv = x > 0 && kt < walk.count, sn = kt + step < walk.count;
             const int np = n0 + kt, ns = np + step;
             const int vs = np % C::kVStages, ks = ns % C::kKStages;
-            if (pv) {
-              if (!(ok = mbar_wait_spin(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag, w.status))) break;
-              if (!(ok = mbar_wait_spin(bar(kBarPHalf + a), mine & 1, abort_flag, w.status))) break;
-            }
-            if (sn && !(ok = mbar_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status))) break;
-            if (!(ok = wait_turn(turn))) break;
-            tc_fence_after();
-            if (pv) {
-              const uint32_t vbase = sbase + C::kOffV + vs * C::kTile;
+            auto k_there = [&]() { return mbar_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status); };
+            auto p_there = [&]() {
+              return mbar_wait_spin(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag, w.status) &&
+                     mbar_wait_spin(bar(kBarPHalf + p_bar(a, mine)), p_phase(mine), abort_flag, w.status);
+            };
+            auto send_s = [&]() {
+              const uint32_t kbase = sbase + C::kOffK + ks * C::kTile, tS = tS0 + kBN * p_bar(a, ns);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t so = (kk >> 2) * C::kSubQ + (kk & 3) * 32, ko = (kk >> 2) * C::kSub + (kk & 3) * 32;
+                umma_f16_ss(tS, smem_desc_sw128(qbase + so, 16, 1024), smem_desc_sw128(kbase + ko, 16, 1024),
+                            idesc_s, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(bar(kBarSFull + p_bar(a, ns)));
+            };
+            auto send_pv = [&]() -> bool {
+              const uint32_t vbase = sbase + C::kOffV + vs * C::kTile, tP = tS0 + kBN * p_bar(a, mine);
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk) {
                 if (kk == kBN / 32) {
-                  if (!(ok = mbar_wait_spin(bar(kBarPFull + a), mine & 1, abort_flag, w.status))) break;
+                  if (!mbar_wait_spin(bar(kBarPFull + p_bar(a, mine)), p_phase(mine), abort_flag, w.status)) return false;
                   tc_fence_after();
                 }
-                umma_f16_ts(tO, tS + kk * 8, smem_desc_sw128(vbase + kk * 16 * 128, C::kSub, 1024), idesc_o,
+                umma_f16_ts(tO, tP + kk * 8, smem_desc_sw128(vbase + kk * 16 * 128, C::kSub, 1024), idesc_o,
                             (x > 1 || kk > 0) ? 1u : 0u);
               }
-              if (!ok) break;
               ++mine;
-            }
-            // S over the columns that these products read as P: the tensor core takes them in order
-            if (sn) {
-              const uint32_t kbase = sbase + C::kOffK + ks * C::kTile;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::kSub + (kk & 3) * 32;
-                umma_f16_ss(tS, smem_desc_sw128(qbase + off, 16, 1024), smem_desc_sw128(kbase + off, 16, 1024),
-                            idesc_s, kk > 0 ? 1u : 0u);
+              return true;
+            };
+            if constexpr (C::kLanes == 2) {
+              if (pv && !(ok = p_there())) break;
+              if (sn && !(ok = k_there())) break;
+              if (!(ok = wait_turn(turn))) break;
+              tc_fence_after();
+              if (pv && !(ok = send_pv())) break;
+              // S over the columns that these products read as P: the tensor core takes them in order
+              if (sn) send_s();
+            } else {
+              // S into the other of two places first: it is done before this tile's softmax is
+              if (sn) {
+                if (!(ok = k_there())) break;
+                tc_fence_after();
+                send_s();
+                umma_commit(bar(kBarKFree + ks));
               }
-              umma_commit(bar(kBarSFull + a));
+              if (pv) {
+                if (!(ok = p_there())) break;
+                tc_fence_after();
+                if (!(ok = send_pv())) break;
+              }
             }
             end_turn();
-            if (sn) release(kBarKFree + ks, ap);
+            if (C::kLanes == 2 && sn) release(kBarKFree + ks, ap);
             if (pv) {
               if (!sn) umma_commit(bar(kBarODone + a));
               release(kBarVFree + vs, ap);
@@ -323,7 +353,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     const int a = warp >> 2;            // the lane
     const int row = threadIdx.x & 127;  // the TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + C::kColS + 128 * a, tO = tmem + lane_base + C::kColO + D * a;
+    const uint32_t tS0 = tmem + lane_base + C::kColS, tO = tmem + lane_base + C::kColO + D * a;
     const float scale_log2 = w.scale * kLog2e;
     // key tiles and this lane's tiles; pieces, those in which lane 1 has a tile, those with lanes apart: so far
     int n0 = 0, mine = 0, done[2] = {0, 0}, joins = 0;
@@ -354,7 +384,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int src = kPer > 0 ? i * kPer + lane / kVecs : i;
         const long long o = __shfl_sync(0xffffffffu, off, src);
         const int rr = (warp & 3) * 32 + src;
-        cp_async16(sbase + C::kOffQ + a * C::kTile + (c >> 3) * C::kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
+        cp_async16(sbase + C::kOffQ + a * C::kTileQ + (c >> 3) * C::kSubQ + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
                    static_cast<const __nv_bfloat16*>(w.q) + (o < 0 ? 0 : o + 8 * c), o >= 0);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -387,9 +417,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       float m_run = -INFINITY;  // maximum that the weights are taken against (log2 units)
       float l_run = 0.f;
       for (int kt = kt0; kt < count; kt += step) {
-        const int k0 = (first + kt) * kBN;
+        const int k0 = (first + kt) * kBN, pb = p_bar(a, mine);
+        const uint32_t tS = tS0 + kBN * pb;
         if (!rehearsal) {
-          if (!(ok = mbar_wait(bar(kBarSFull + a), mine & 1, abort_flag, w.status))) break;
+          if (!(ok = mbar_wait(bar(kBarSFull + pb), p_phase(mine), abort_flag, w.status))) break;
           ++mine;
           tc_fence_after();
           if (k0 + kBN > hi) {
@@ -398,7 +429,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             // the tile write the same zeros)
             const int n = n0 + kt, s = n % C::kVStages;
             if (!(ok = mbar_wait(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag, w.status))) break;
-            if (k0 + row >= hi) {
+            if (row < kBN && k0 + row >= hi) {
 #pragma unroll 1
               for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4*>(smem + C::kOffV + s * C::kTile + (c >> 3) * C::kSub + row * 128 +
@@ -409,8 +440,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           if (!warp_valid) {  // no row of this warp counts: its P may be anything
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(bar(kBarPHalf + a));
-              mbar_arrive(bar(kBarPFull + a));
+              mbar_arrive(bar(kBarPHalf + pb));
+              mbar_arrive(bar(kBarPFull + pb));
             }
             continue;
           }
@@ -418,19 +449,19 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         float s[kBN];
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const int cols = lim - k0;  // valid columns: c < cols
-        auto take_half = [&](int base, uint32_t (&ra)[32], uint32_t (&rb)[32]) {
+        auto take = [&](int base, uint32_t (&ra)[32], uint32_t (&rb)[32]) {  // 64 columns
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             s[base + e] = __uint_as_float(ra[e]);
             s[base + 32 + e] = __uint_as_float(rb[e]);
           }
-          if (cols < base + kBN / 2) {
+          if (cols < base + 64) {
 #pragma unroll
-            for (int c = base; c < base + kBN / 2; ++c)
+            for (int c = base; c < base + 64; ++c)
               if (c >= cols) s[c] = -INFINITY;
           }
 #pragma unroll
-          for (int c = base; c < base + kBN / 2; c += 8) {
+          for (int c = base; c < base + 64; c += 8) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) mp[x] = fmax3(mp[x], s[c + x], s[c + 4 + x]);
           }
@@ -442,13 +473,17 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           tmem_wait_ld();
           reg_dep32(ra);
           reg_dep32(rb);
-          tmem_ld32(tS + 64, rc);
-          tmem_ld32(tS + 96, rd);
-          take_half(0, ra, rb);
-          tmem_wait_ld();
-          reg_dep32(rc);
-          reg_dep32(rd);
-          take_half(kBN / 2, rc, rd);
+          if constexpr (kBN == 128) {
+            tmem_ld32(tS + 64, rc);
+            tmem_ld32(tS + 96, rd);
+          }
+          take(0, ra, rb);
+          if constexpr (kBN == 128) {
+            tmem_wait_ld();
+            reg_dep32(rc);
+            reg_dep32(rd);
+            take(64, rc, rd);
+          }
         }
         const float m_tile = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * scale_log2;
         const bool any = __any_sync(0xffffffffu, m_tile > m_run + kRescaleLog2);
@@ -462,7 +497,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         uint64_t ps2[2] = {0ull, 0ull};
         const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
         const uint64_t shift2 = f2_pack(-m_use, -m_use);
-        // P of columns cb .. cb + 63 over the TMEM columns cb / 2 .. (S is in registers)
+        // P of half of the columns, cb and up, over the TMEM columns cb / 2 .. (S is in registers)
         auto exp_cols = [&](int cb) {
 #pragma unroll
           for (int q = cb; q < cb + kBN / 2; q += 32) {
@@ -482,7 +517,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         exp_cols(0);
         if (any && (kt > kt0 || rehearsal)) {
           // O is rescaled before this tile's products; the last tile's are
-          // done, since this S was issued after them
+          // done, since this S was issued after them (with one lane: waited for)
+          if (C::kLanes == 1 && !rehearsal) {
+            const int n = n0 + kt - 1;
+            if (!(ok = mbar_wait(bar(kBarVFree + n % C::kVStages), (n / C::kVStages) & 1, abort_flag, w.status))) break;
+            tc_fence_after();
+          }
           const uint64_t alpha2 = f2_pack(alpha, alpha);
 #pragma unroll 1
           for (int c = 0; c < D / 32; c += 2) {
@@ -509,7 +549,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPHalf + a));
+        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPHalf + pb));
         exp_cols(kBN / 2);
         {
           float a0, a1, b0, b1;
@@ -520,7 +560,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPFull + a));
+        if (lane == 0 && !rehearsal) mbar_arrive(bar(kBarPFull + pb));
       }
       if (!ok) break;
       if (rehearsal) {
@@ -560,7 +600,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // Lanes apart: their results of a row join here, each lane finishing
         // half of the columns.  A thread of either lane sees the row's both O in
         // TMEM; (m, l) cross over there, too, in columns that P has left.
-        tmem_st2(tS, __float_as_uint(m_run), __float_as_uint(l_run));
+        tmem_st2(tS0 + kBN * a, __float_as_uint(m_run), __float_as_uint(l_run));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -569,7 +609,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tc_fence_after();
         if (warp_valid) {
           uint32_t xm, xl;
-          tmem_ld2(tmem + lane_base + C::kColS + 128 * (1 - a), xm, xl);
+          tmem_ld2(tS0 + kBN * (1 - a), xm, xl);
           const float om = __uint_as_float(xm), ol = __uint_as_float(xl);
           const float top = fmaxf(m_run, om);
           const float base = top == -INFINITY ? 0.f : top;
@@ -626,8 +666,8 @@ template <int D>
 cudaError_t run(const PagedWork& w, cudaStream_t stream) {
   using C = PrefixCfg<D>;
   CUtensorMap mk, mv;
-  if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != CUDA_SUCCESS ||
-      encode_pages_map(&mv, w.p.v_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) != CUDA_SUCCESS)
+  if (encode_pages_map(&mk, w.p.k_pages, w.p, C::kBN, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != CUDA_SUCCESS ||
+      encode_pages_map(&mv, w.p.v_pages, w.p, C::kBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   cudaError_t e =
       cudaFuncSetAttribute(paged_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);

@@ -112,9 +112,9 @@ cudaError_t launch_paged_attention(const PagedWork& w, const PagedShape& shape, 
 // TMA view of a page array; one box is 128 bytes of up to `tile` tokens of a page.
 CUresult encode_pages_map(CUtensorMap* map, const void* base, const PagedArgs& p, int tile, CUtensorMapDataType type);
 
-// The prefixes' list on tcgen05 (bf16): key tiles of 128, row tiles of up to
-// 256 (128 for d 256), one CTA an SM.
-constexpr int kPrefixBN = 128;
+// The prefixes' list on tcgen05 (bf16): key tiles of 128 and row tiles of up to
+// 256, for d 256 of 64 and 128; one CTA an SM.
+constexpr int paged_prefix_keys(int head_dim) { return head_dim == 256 ? 64 : 128; }
 constexpr int paged_prefix_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 cudaError_t launch_paged_prefix(const PagedWork& w, cudaStream_t stream);
 

@@ -13,7 +13,7 @@ from tests import paged_work_model as M
 @pytest.mark.parametrize("seed", range(250))
 def test_pieces_cover_and_partials_are_apart(seed):
     r = random.Random(seed)
-    bn, most = r.choice([(64, 64), (32, 16), (128, 256), (128, 128)])
+    bn, most = r.choice([(64, 64), (32, 16), (128, 256), (64, 128)])
     hkv, ctas = r.choice([1, 2, 3, 8]), r.choice([1, 7, 148, 296, 444])
     items = []
     for _ in range(r.randint(1, 30)):
