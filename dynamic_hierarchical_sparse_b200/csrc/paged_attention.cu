@@ -23,10 +23,9 @@
 // is latency: the first pass over the code, one round of loads, the join.
 //
 // paged_f32_kernel (fp32): the same with 32-key tiles and 16 rows, on tf32
-// fragments in pairs.  Bound by its products: an m16n8k8 takes 8 cycles of a
-// quarter of an SM whatever of its 16 rows is in use, and a product is three of
-// them.  Measured: 4 sequences on 14117 keys, 32 + 8 heads: 75 us with d 256, 42
-// with d 128 (231 and 116 MB).
+// fragments in pairs.  Bound by latency, of loads and of its own instructions.
+// Measured: 4 sequences on 14117 keys, 32 + 8 heads: 65 us with d 256, 38 with d
+// 128 (231 and 116 MB).
 #include "launchers.h"
 #include "paged.cuh"
 
@@ -502,7 +501,9 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 // fp32 products on tf32 fragments, each number as the sum of two: x = h + l with
 // h the tf32 (11 bits) nearest to x and l the tf32 nearest to x - h, so h + l is
 // x to 2^-22, and a b = h h' + h l' + l h' to about 2^-21 of |a b|, accumulated in
-// fp32.  (The same in FFMA is bound by shared memory: 16 rows are too few for a
+// fp32.  Rounding by two integer instructions (an infinity stays one, a NaN becomes
+// NaN or leaves it to l) takes those calls from 74 and 42 us, with the conversion's
+// own, to 65 and 38.  (The same in FFMA is bound by shared memory: 16 rows are too few for a
 // register block that would feed it.)  A tile is 16 rows and 32 keys; the four
 // warps split the keys.
 constexpr int kFBN = 32;    // keys a tile
@@ -525,10 +526,8 @@ struct F32Cfg {
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ uint32_t to_tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
+__device__ __forceinline__ uint32_t to_tf32(float x) {  // to the nearest of 11 significant bits
+  return (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
 }
 __device__ __forceinline__ void split_tf32(float x, uint32_t& h, uint32_t& l) {
   h = to_tf32(x);
@@ -732,7 +731,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int b = paged_seq_of(w.p, t);
   // a row's partials of one item: rows at + j * kStep for j < count
   struct Place {
-    int seg, nt, ts, in_tile, j, n;  // segment, its key tiles, log2 rows a tile, row in the tile; item of its list, items
+    int seg, nt, ts, in_tile;  // segment, its key tiles, log2 rows a tile, row in the tile
+    int j, n;                  // item of its list, items
   };
   auto place = [&](auto span, const PagedList& l, int i) -> Place {
     using Span = decltype(span);
@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   Place pp{0, 0, 0, 0, 0, 0};
   if (w.p.num_groups > 0) {
     const int g = paged_group_of(w.p, b);
-    pp = own_list ? place(PagedSpan<paged_prefix_keys(D), kPrefixRows>(), w.prefix, g) : place(PagedSpan<BN, kMax>(), w.list, g);
+    pp = own_list ? place(PagedSpan<paged_prefix_keys(D), kPrefixRows>(), w.prefix, g)
+                  : place(PagedSpan<BN, kMax>(), w.list, g);
   }
   const Place po = place(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
   wait_for_previous();
@@ -883,7 +884,8 @@ cudaError_t run_mma(PagedWork w, cudaStream_t stream) {
   if (encode_pages_map(&mk, w.p.k_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != CUDA_SUCCESS ||
       encode_pages_map(&mv, w.p.v_pages, w.p, kBN, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, kMax>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_mma_kernel<D, kMax>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;

@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             const bool pv = x > 0 && kt < walk.count, sn = kt + step < walk.count;
             const int np = n0 + kt, ns = np + step;
             const int vs = np % C::kVStages, ks = ns % C::kKStages;
-            auto k_there = [&]() { return mbar_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status); };
+            auto k_there = [&]() {
+              return mbar_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status);
+            };
             auto p_there = [&]() {
               return mbar_wait_spin(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag, w.status) &&
                      mbar_wait_spin(bar(kBarPHalf + p_bar(a, mine)), p_phase(mine), abort_flag, w.status);
@@ -300,7 +302,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk) {
                 if (kk == kBN / 32) {
-                  if (!mbar_wait_spin(bar(kBarPFull + p_bar(a, mine)), p_phase(mine), abort_flag, w.status)) return false;
+                  if (!mbar_wait_spin(bar(kBarPFull + p_bar(a, mine)), p_phase(mine), abort_flag, w.status))
+                    return false;
                   tc_fence_after();
                 }
                 umma_f16_ts(tO, tP + kk * 8, smem_desc_sw128(vbase + kk * 16 * 128, C::kSub, 1024), idesc_o,
