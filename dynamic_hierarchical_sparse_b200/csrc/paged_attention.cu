@@ -24,7 +24,7 @@
 //
 // paged_f32_kernel (fp32): the same with 32-key tiles and 16 rows, on tf32
 // fragments in pairs.  Bound by latency, of loads and of its own instructions.
-// Measured: 4 sequences on 14117 keys, 32 + 8 heads: 65 us with d 256, 38 with d
+// Measured: 4 sequences on 14117 keys, 32 + 8 heads: 64 us with d 256, 38 with d
 // 128 (231 and 116 MB).
 #include "launchers.h"
 #include "paged.cuh"
@@ -499,13 +499,14 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 
 // ------------------------------------------------------------------ fp32
 // fp32 products on tf32 fragments, each number as the sum of two: x = h + l with
-// h the tf32 (11 bits) nearest to x and l the tf32 nearest to x - h, so h + l is
-// x to 2^-22, and a b = h h' + h l' + l h' to about 2^-21 of |a b|, accumulated in
-// fp32.  Rounding by two integer instructions (an infinity stays one, a NaN becomes
-// NaN or leaves it to l) takes those calls from 74 and 42 us, with the conversion's
-// own, to 65 and 38.  (The same in FFMA is bound by shared memory: 16 rows are too few for a
-// register block that would feed it.)  A tile is 16 rows and 32 keys; the four
-// warps split the keys.
+// h the tf32 (11 bits) nearest to x and l = x - h, 12 bits, without its last where
+// it has them all: h + l is x to 2^-23, and a b = h h' + h l' + l h' to about 2^-21
+// of |a b|, accumulated in fp32.  The split takes integer instructions, which takes
+// 4 sequences on 14117 keys from 74 to 64 us with d 256 and from 42 to 38 with d
+// 128 against the conversion's own; an infinity has a NaN for l, and a NaN whose
+// bits the rounding carries past the sign leaves itself in l.  (The same in FFMA is
+// bound by shared memory: 16 rows are too few for a register block that would feed
+// it.)  A tile is 16 rows and 32 keys; the four warps split the keys.
 constexpr int kFBN = 32;    // keys a tile
 constexpr int kFRows = 16;  // rows a tile
 
@@ -526,12 +527,9 @@ struct F32Cfg {
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ uint32_t to_tf32(float x) {  // to the nearest of 11 significant bits
-  return (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-}
 __device__ __forceinline__ void split_tf32(float x, uint32_t& h, uint32_t& l) {
-  h = to_tf32(x);
-  l = to_tf32(x - __uint_as_float(h));
+  h = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  l = __float_as_uint(x - __uint_as_float(h)) & 0xffffe000u;
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(

@@ -383,6 +383,29 @@ def test_paged_attention_extreme_logits(dt):
     assert np.all(np.abs(_np(out)[2] - want[2]) <= bound[2])
 
 
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, 0x7FC00000, 0x7F810000, -1, -0x7F0000])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_paged_attention_any_nan(dt, bits):
+    """Every NaN, whatever its bits, in a query, key or value makes the rows that meet it NaN."""
+    def nan(dtype):
+        if dtype == F32:
+            return torch.tensor([bits], dtype=torch.int32).view(F32)[0]
+        t = torch.tensor([bits >> 16], dtype=torch.int16).view(BF16)[0]
+        return t if dtype == BF16 else t.to(dtype)
+    st = C.Step(31, dt, 8, 2, 64, 16, [1, 1, 2], [40, 33, 90])
+    clean, _ = _attend(st)
+    st.q[1, 3, 7] = nan(st.q.dtype)                                # a query head of sequence 1
+    st.k_pages[st.table[0, 1], 1, 3, 9] = nan(st.k_pages.dtype)    # a key of sequence 0, heads 4 to 7
+    st.v_pages[st.table[2, 2], 0, 5, 11] = nan(st.v_pages.dtype)   # a value of sequence 2, heads 0 to 3
+    assert st.q[1, 3, 7].isnan() and st.k_pages[st.table[0, 1], 1, 3, 9].isnan()
+    got, lse = _attend(st)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[1, 3] = hit[0, 4:] = hit[2:, :4, 11] = True
+    assert torch.equal(torch.isnan(got), hit)
+    assert torch.equal(torch.isnan(lse), (hit.all(-1)))
+    assert torch.equal(got[~hit], clean[~hit])
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 def test_paged_attention_reports_bad_tables(dt):
     for change in ("page", "negative", "long", "short", "prefix"):
