@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       if (rehearsal) {
         rehearsal = false;
         wait_for_previous();
-        __syncthreads();  // the schedule is there; what this round wrote to TMEM is behind tc_fence_before
+        __syncthreads();  // the schedule is there; what the rehearsal wrote to TMEM is behind tc_fence_before
         if (!walk.init(&w.p, gh, w.prefix, sc)) break;
         send_q(walk);
         continue;
