@@ -508,7 +508,7 @@ class _on_device:
             torch.cuda.set_device(self.before)
 
 
-def _call(fn, name: str, index: int, *args) -> None:
+def _call(fn, name: str, index: int, args: tuple) -> None:
     """fn(*args) with device `index` current; raises on an error status."""
     if _current_device() == index:
         code = fn(*args)
@@ -524,6 +524,7 @@ def _stream_on(stream, index: int) -> int:
 
 
 _NO_TOKENS = _Tokens(None, 0)  # passed by value, never written
+_I32 = torch.int32
 
 
 def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dtype: torch.dtype, tokens: int,
@@ -532,26 +533,29 @@ def _tokens(t: Optional[torch.Tensor], name: str, heads: int, head_dim: int, dty
     tensor), on CUDA device `index`."""
     if t is None:
         return _NO_TOKENS
-    if t.ndim == 3:
-        n, h, d = t.shape
-        st, sh, sd = t.stride()
-        if (h == heads and d == head_dim and n >= tokens and sd == 1 and (sh == d or h == 1) and t.dtype is dtype
-                and t.get_device() == index and (st >= h * d or n <= 1)):
-            return _Tokens(t.data_ptr(), st if n > 1 else h * d)
+    shape = t.shape
+    if len(shape) == 3 and t.dtype is dtype and t.get_device() == index:
+        n, h, d = shape
+        if h == heads and d == head_dim and n >= tokens:
+            if t.is_contiguous():
+                return _Tokens(t.data_ptr(), h * d)
+            st, sh, sd = t.stride()
+            if sd == 1 and (sh == d or h == 1) and (st >= h * d or n <= 1):
+                return _Tokens(t.data_ptr(), st if n > 1 else h * d)
     # what of it is wrong
     if t.get_device() != index:
         raise ValueError("%s must be a CUDA tensor on device %d, got %s" % (name, index, t.device))
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.ndim != 3 or n < tokens or h != heads or d != head_dim:
-        raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(t.shape)))
+    if len(shape) != 3 or n < tokens or h != heads or d != head_dim:
+        raise ValueError("%s must be [>= %d, %d, %d], got %s" % (name, tokens, heads, head_dim, tuple(shape)))
     if sd != 1 or (sh != d and h > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % name)
     raise ValueError("the tokens of %s overlap (a broadcast tensor must be expanded to memory of its own)" % name)
 
 
 def _int32(t: torch.Tensor, name: str, shape, index: int) -> None:
-    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
+    if t.dtype is _I32 and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
         return
     if t.get_device() != index or index < 0:
         raise ValueError("%s must be a CUDA tensor on device %d" % (name, index))
@@ -614,10 +618,10 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
             k_out = torch.empty(T, hk, d, dtype=dtype, device=x.device)
     if stream is not None:
         _enter(stream)
-    _call(rope.fn, "dhsa_rope", dev, rope.ref, _dtype_code(x), d, T, positions.data_ptr(),
-          _tokens(q, "q", hq, d, dtype, T, dev), hq, _tokens(q_out, "q_out", hq, d, dtype, T, dev),
-          _tokens(k, "k", hk, d, dtype, T, dev), hk, _tokens(k_out, "k_out", hk, d, dtype, T, dev),
-          _stream_on(stream, dev))
+    _call(rope.fn, "dhsa_rope", dev,
+          (rope.ref, _dtype_code(x), d, T, positions.data_ptr(), _tokens(q, "q", hq, d, dtype, T, dev), hq,
+           _tokens(q_out, "q_out", hq, d, dtype, T, dev), _tokens(k, "k", hk, d, dtype, T, dev), hk,
+           _tokens(k_out, "k_out", hk, d, dtype, T, dev), _stream_on(stream, dev)))
     if stream is not None:
         _leave(stream)
     return q_out, k_out
@@ -736,10 +740,10 @@ class KvAppender:
         if positions is not None:
             _int32(positions, "positions", (T,), dev)
             pos = positions.data_ptr()
-        _call(self._fn, "dhsa_kv_append", dev, *self._fixed, pos, _tokens(k, "k", hk, d, dt, T, dev),
-              _tokens(v, "v", hk, d, dt, T, dev), _tokens(k_out, "k_out", hk, d, dt, T, dev),
-              _tokens(q, "q", hq, d, dt, T, dev), _tokens(q_out, "q_out", hq, d, dt, T, dev), hq, self._ws, 256,
-              _stream_on(stream, dev))
+        _call(self._fn, "dhsa_kv_append", dev,
+              (*self._fixed, pos, _tokens(k, "k", hk, d, dt, T, dev), _tokens(v, "v", hk, d, dt, T, dev),
+               _tokens(k_out, "k_out", hk, d, dt, T, dev), _tokens(q, "q", hq, d, dt, T, dev),
+               _tokens(q_out, "q_out", hq, d, dt, T, dev), hq, self._ws, 256, _stream_on(stream, dev)))
         return q_out, k_out
 
     def status(self, stream=None) -> int:
@@ -796,9 +800,9 @@ class PagedAttention:
                     or lse.dim() != 2 or lse.shape[0] < T or lse.shape[1] != hq:
                 raise ValueError("lse must be a contiguous float32 [>= %d, %d] tensor on device %d" % (T, hq, dev))
             lse_ptr = lse.data_ptr()
-        _call(self._fn, "dhsa_paged_attention", dev, *self._fixed, _tokens(q, "q", hq, d, dt, T, dev), hq,
-              0.0 if scale is None else scale, _tokens(out, "out", hq, d, dt, T, dev), lse_ptr, self._ws,
-              self._ws_bytes, _stream_on(stream, dev))
+        _call(self._fn, "dhsa_paged_attention", dev,
+              (*self._fixed, _tokens(q, "q", hq, d, dt, T, dev), hq, 0.0 if scale is None else scale,
+               _tokens(out, "out", hq, d, dt, T, dev), lse_ptr, self._ws, self._ws_bytes, _stream_on(stream, dev)))
         return out
 
     def status(self, stream=None) -> int:
