@@ -820,24 +820,30 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const Place po = place(PagedSpan<BN, kMax>(), w.list, w.p.num_groups + b);
   wait_for_previous();
   const bool live = h < w.num_q_heads;
-  auto first_row = [&](const Place& p, const PagedList& l, int step, int& count) -> int {
-    count = 0;
-    if (p.nt == 0 || limit <= 0 || !live) return 0;
-    const int how = l.items[p.n + 1];
-    const PagedCut cut{l.items[p.n], max(how, 0), max(-how, 0), l.by_ctas};
-    // (the prefixes' own list has no extra tiles: there a tile is one)
-    const int wt = cut.tile_units<kMax>(p.ts);
-    const int u0 = l.items[p.j] + p.seg * cut.padded(p.nt, wt);
-    const int row = l.items[p.n + 2 + p.j];
-    const int c0 = cut.owner(u0), c1 = cut.owner(u0 + (p.nt - 1) * wt);
-    count = c1 - c0 + 1;
-    return paged_part_row(c0, step, row, p.seg, p.ts) + p.in_tile;
-  };
+  // the first and last partial of the prefix's segment (lanes 0 and 1 of four) and of
+  // the row's own (2 and 3), found side by side: divisions are long code to fetch
   const PagedList& pl = own_list ? w.prefix : w.list;
   const int pstep = own_list ? kPrefixRows : kMax;
-  int pcount, ocount;
-  const int pfirst = first_row(pp, pl, pstep, pcount);
-  const int ofirst = first_row(po, w.list, kMax, ocount);
+  int first, owner;
+  {
+    const bool own = (lane & 2) != 0, last = (lane & 1) != 0;
+    const int* items = own ? w.list.items : pl.items;
+    const int seg = own ? po.seg : pp.seg, nt = own ? po.nt : pp.nt, ts = own ? po.ts : pp.ts;
+    const int j = own ? po.j : pp.j, n = own ? po.n : pp.n;
+    const int how = items[n + 1];
+    PagedCut cut{items[n], max(how, 0), max(-how, 0), w.list.by_ctas};
+    if (!own) cut.by_ctas = pl.by_ctas;
+    // (the prefixes' own list has no extra tiles: there a tile is one unit)
+    const int wt = cut.tile_units<kMax>(ts);
+    const int u0 = items[j] + seg * cut.padded(nt, wt);
+    owner = cut.owner(last ? u0 + (nt - 1) * wt : u0);
+    first = paged_part_row(owner, own ? kMax : pstep, items[n + 2 + j], seg, ts) + (own ? po.in_tile : pp.in_tile);
+  }
+  const int pfirst = __shfl_sync(0xffffffffu, first, 0), ofirst = __shfl_sync(0xffffffffu, first, 2);
+  const int spans = __shfl_down_sync(0xffffffffu, owner, 1) - owner + 1;
+  const bool sees = limit > 0 && live;
+  const int pcount = sees && pp.nt > 0 ? __shfl_sync(0xffffffffu, spans, 0) : 0;
+  const int ocount = sees && po.nt > 0 ? __shfl_sync(0xffffffffu, spans, 2) : 0;
   const int all = pcount + ocount;
   float m = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
