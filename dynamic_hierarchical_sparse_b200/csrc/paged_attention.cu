@@ -339,26 +339,30 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
   const int h = k.h, rows = k.rows(), row0 = k.row0();
   const float scale_log2 = w.scale * kLog2e;
 
-  // this thread's two rows: lane / 4 and + 8 of the warp's 16
+  // the warp's 16 rows, one a lane (one copy of the code for both of a thread's rows)
+  int my_lim = 0;
+  long long my_q = -1;
+  {
+    const int r = row0 + wm * 16 + (lane & 15);
+    if (r < rows) {
+      const int tr = w.by_group(r), t = k.it.t0 + tr;
+      const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
+      my_lim = min(k.it.hi, paged_limit(w.p, b, t));
+      my_q = t * w.q_stride + static_cast<long long>((h - tr) * gh + r) * D;
+    }
+  }
+  // the smallest and largest limit over the valid rows
+  const int lim_min = __reduce_min_sync(0xffffffffu, my_q < 0 ? INT_MAX : my_lim);
+  const int lim_max = __reduce_max_sync(0xffffffffu, my_lim);
+  // this thread's two rows: lane / 4 and + 8
   int lim[2];
   const __nv_bfloat16* qrow[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int r = row0 + wm * 16 + (lane >> 2) + 8 * e;
-    lim[e] = 0;
-    qrow[e] = nullptr;
-    if (r < rows) {
-      const int tr = w.by_group(r), t = k.it.t0 + tr;
-      const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
-      lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
-      qrow[e] = static_cast<const __nv_bfloat16*>(w.q) + t * w.q_stride +
-                static_cast<long long>((h - tr) * gh + r) * D;
-    }
+    lim[e] = __shfl_sync(0xffffffffu, my_lim, (lane >> 2) + 8 * e);
+    const long long at = __shfl_sync(0xffffffffu, my_q, (lane >> 2) + 8 * e);
+    qrow[e] = at < 0 ? nullptr : static_cast<const __nv_bfloat16*>(w.q) + at;
   }
-  // the warp's smallest and largest limit over its valid rows
-  int lim_min = min(qrow[0] ? lim[0] : INT_MAX, qrow[1] ? lim[1] : INT_MAX), lim_max = max(lim[0], lim[1]);
-  lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-  lim_max = __reduce_max_sync(0xffffffffu, lim_max);
 
   uint32_t qf[D / 16][4];
 #pragma unroll
@@ -635,17 +639,16 @@ __device__ __forceinline__ bool f32_piece(const PagedWork& w, const PagedWalk<kF
     *reinterpret_cast<uint4*>(qh + tr * C::kQStride + 4 * c) = vh;
     *reinterpret_cast<uint4*>(ql + tr * C::kQStride + 4 * c) = vl;
   }
-  int lim[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = row0 + (lane >> 2) + 8 * e;
-    lim[e] = 0;
+  int my_lim = 0;  // the 16 rows, one a lane
+  {
+    const int r = row0 + (lane & 15);
     if (r < rows) {
       const int t = k.it.t0 + w.by_group(r);
       const int b = k.i < w.p.num_groups ? paged_seq_of(w.p, t) : k.it.row;
-      lim[e] = min(k.it.hi, paged_limit(w.p, b, t));
+      my_lim = min(k.it.hi, paged_limit(w.p, b, t));
     }
   }
+  const int lim[2] = {__shfl_sync(0xffffffffu, my_lim, lane >> 2), __shfl_sync(0xffffffffu, my_lim, (lane >> 2) + 8)};
   float o[D / 8][4];
 #pragma unroll
   for (int j = 0; j < D / 8; ++j)
