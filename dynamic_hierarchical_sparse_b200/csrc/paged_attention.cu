@@ -790,6 +790,15 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
 // looked up, when the kernel before ends.  The whole call with 4 / 1, in us: 128
 // rows 10.3 / 11.4, 1024 rows 59.9 / 62.5, 1536 rows 135.9 / 134.3, 2048 rows
 // 188.1 / 187.6.
+template <int N>
+struct __align__(N >= 4 ? 16 : 8) Cols {  // consecutive numbers, read and written together
+  float x[N];
+};
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+
 template <int D, typename T, int BN, int kMax, int WARPS>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedWork w) {
   let_next_start();
@@ -848,14 +857,15 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int pcount = sees && pp.nt > 0 ? __shfl_sync(0xffffffffu, spans, 0) : 0;
   const int ocount = sees && po.nt > 0 ? __shfl_sync(0xffffffffu, spans, 2) : 0;
   const int all = pcount + ocount;
-  float m = -INFINITY, sum = 0.f, acc[kCols];
+  float m = -INFINITY, sum = 0.f;
+  __align__(16) float acc[kCols];  // columns lane * kCols and on
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-  constexpr int kBatch = WARPS == 4 || D == 256 ? 4 : 8;  // partials in flight a warp
+  constexpr int kBatch = D == 256 ? 4 : 8;  // partials in flight a warp
 #pragma unroll 1
   for (int j0 = part; j0 < all; j0 += WARPS * kBatch) {
     float2 ml[kBatch];
-    float x[kBatch][kCols];
+    __align__(16) float x[kBatch][kCols];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int j = j0 + WARPS * i;
@@ -867,8 +877,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         const int r = pre ? pfirst + j * pstep : ofirst + (j - pcount) * kMax;
         ml[i] = (pre ? pl.part_ml : w.list.part_ml)[r];
         const float* o = (pre ? pl.part_o : w.list.part_o) + static_cast<long long>(r) * D;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) x[i][c] = o[c * 32 + lane];
+        *reinterpret_cast<Cols<kCols>*>(x[i]) = *reinterpret_cast<const Cols<kCols>*>(o + lane * kCols);
       }
     }
     float top = m;
@@ -889,10 +898,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     }
   }
   if constexpr (WARPS == 4) {
-    __shared__ float acc_s[4][D];
+    __shared__ __align__(16) float acc_s[4][D];
     __shared__ float2 ml_s[4];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc_s[warp][c * 32 + lane] = acc[c];
+    *reinterpret_cast<Cols<kCols>*>(&acc_s[warp][lane * kCols]) = *reinterpret_cast<const Cols<kCols>*>(acc);
     if (lane == 0) ml_s[warp] = make_float2(m, sum);
     __syncthreads();
     if (warp != 0) return;
@@ -911,14 +919,15 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     for (int c = 0; c < kCols; ++c) {
       acc[c] = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[c] = fmaf(acc_s[x][c * 32 + lane], f[x], acc[c]);
+      for (int x = 0; x < 4; ++x) acc[c] = fmaf(acc_s[x][lane * kCols + c], f[x], acc[c]);
     }
   }
   if (!live) return;
   T* out = static_cast<T*>(w.out) + t * w.out_stride + static_cast<long long>(h) * D;
   const float inv = limit > 0 ? 1.f / sum : 0.f;  // a row that sees no key: acc is 0
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) out[c * 32 + lane] = static_cast<T>(acc[c] * inv);
+  for (int c = 0; c < kCols; c += 2)
+    store2(out + lane * kCols + c, acc[c] * inv, acc[c + 1] * inv);
   if (w.lse != nullptr && lane == 0)
     w.lse[static_cast<long long>(t) * w.num_q_heads + h] = limit > 0 ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
