@@ -96,8 +96,8 @@ __host__ __device__ __forceinline__ int paged_tile_shift(int rows) {
 // Units that a key tile counts, by log2 of its rows (see PagedCut): in the kernel
 // with tiles of up to 64 rows one of 64 takes about 2.6 times as long as one of
 // 16.  Counting every tile alike / 1, 2, 3, in us (32 + 8 heads of 128, up to 512
-// own keys): 16 sequences on 1024 shared keys 21.0 / 17.6, on 8192 32.1 / 29.4, 32
-// on 2048 32.1 / 24.0; of d 256, 16 on 1000 45.0 / 29.9.
+// own keys): 16 sequences on 1024 shared keys 18.8 / 15.4, on 8192 29.4 / 26.5, 32
+// on 2048 29.7 / 22.9; of d 256, 16 on 1000 43.4 / 28.1.
 template <int kMax>
 __host__ __device__ __forceinline__ constexpr int paged_tile_units(int ts) {
   return kMax != 64 ? 1 : ts - 3;

@@ -19,7 +19,7 @@
 // Q stays in registers, P goes from the S fragments straight into the A
 // operand of P V (f16, as V).  Measured: 48 unshared sequences of 100 to 8192
 // keys, 32 + 8 heads of 128: 135 us for 839 MB, 6.2 TB/s (0.95 of the measured copy
-// rate), of which the join has 4.  A short call (4 sequences, 128 rows, 10.3 us)
+// rate), of which the join has 4.  A short call (4 sequences, 128 rows, 9.3 us)
 // is latency: the first pass over the code, one round of loads, the join.
 //
 // paged_f32_kernel (fp32): the same with 32-key tiles and 16 rows, on tf32
@@ -39,11 +39,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // long: rows x Hkv x d x the tokens that a table row has room for (their lengths
 // are on the device) of 2^30 or more.  That kernel costs a few us more to start
 // and end; 32 + 8 heads of 128, page 16, up to 512 own keys, one kernel / two, in
-// us: 16 sequences on 1024 keys 17.4 / 24.1, on 16384 38.7 / 38.4, 32 on 2048
-// 24.2 / 32.5, on 8192 39.1 / 37.5, 12 on 32768 56.5 / 49.9, 32 on 32768 103 /
-// 60, 64 on 131072 591 / 189; 64 of d 64 on 1024 24.7 / 29.6, 16 of d 256 on
-// 8000 52.4 / 42.0; 12 sequences of 5 tokens in two groups, 8 + 4 heads of 256,
-// on 4097 52.0 / 39.2.
+// us: 16 sequences on 1024 keys 15.5 / 22.5, on 16384 36.1 / 36.0, 32 on 2048
+// 22.9 / 30.2, on 8192 37.6 / 35.0, 12 on 32768 53.8 / 47.5, 32 on 32768 100 /
+// 57.7, 64 on 131072 587 / 188; 64 of d 64 on 1024 22.6 / 28.3, 16 of d 256 on
+// 8000 50.5 / 40.7; 12 sequences of 5 tokens in two groups, 8 + 4 heads of 256,
+// on 4097 50.1 / 38.5.
 constexpr int kOwnPrefixRows = 32;
 constexpr long long kOwnPrefixWork = 1ll << 30;
 
@@ -788,8 +788,8 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
 // rows are few, so that a row's partials are all in flight at once, and 1 where they
 // are many, so that the CTAs are few enough to be there, their places
 // looked up, when the kernel before ends.  The whole call with 4 / 1, in us: 128
-// rows 10.3 / 11.4, 1024 rows 59.9 / 62.5, 1536 rows 135.9 / 134.3, 2048 rows
-// 188.1 / 187.6.
+// rows 9.3 / 11.1, 512 rows 15.6 / 17.1, 1024 rows 57.6 / 61.9, 1536 rows 138.4 /
+// 136.3, 2048 rows 187.0 / 187.9.
 template <int N>
 struct __align__(N >= 4 ? 16 : 8) Cols {  // consecutive numbers, read and written together
   float x[N];
@@ -861,7 +861,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   __align__(16) float acc[kCols];  // columns lane * kCols and on
 #pragma unroll
   for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
-  constexpr int kBatch = D == 256 ? 4 : 8;  // partials in flight a warp
+  // partials in flight a warp (4 / 8, in us: 4 short answers 9.6 / 9.2, 16 to 8192
+  // tokens 27.3 / 26.4; d 256, 5 tokens on 4097 keys, 38.2 / 40.4)
+  constexpr int kBatch = D == 256 ? 4 : 8;
 #pragma unroll 1
   for (int j0 = part; j0 < all; j0 += WARPS * kBatch) {
     float2 ml[kBatch];
@@ -941,12 +943,13 @@ int sm_count() {
 }
 
 // Key tiles that a segment counts beside its own, for its Q, its first tile's
-// latency and its end.  With 0 / 1 / 2 / 3 / 4, in us: 32 answers to 32K 67.0 /
-// 60.2 / 59.8 / 60.5 / 60.8, 5 tokens on 4097 keys, d 256, 47.0 / 43.4 / 41.5 /
-// 42.3 / 43.0, fp32 with 14117 shared and up to 13 own tokens 138 / 78 / 75 / 74
-// / 76; with 1 / 2 / 3: 7 tokens of 16 unshared sequences 28.6 / 26.7 / 25.8, 16
-// answers to 8192 tokens 31.1 / 29.4 / 28.7, 32 to 2048 25.7 / 24.0 / 25.7.
+// latency and its end.  With 1 / 2 / 3 / 4, in us: 32 answers to 32K 57.9 / 57.7 /
+// 58.3 / 58.6, 5 tokens on 4097 keys, d 256, 39.5 / 38.6 / 39.3 / 40.3, 7 tokens of
+// 16 unshared sequences 28.2 / 26.5 / 26.0 / 26.9, 16 answers to 8192 tokens 28.3 /
+// 26.5 / 26.1 / 26.1, 32 to 2048 24.1 / 22.9 / 23.7 / 23.6, fp32 with 14117 shared
+// and up to 13 own tokens 67.8 / 64.6 / 65.2 / 66.5.
 constexpr int kSegmentTiles = 2;
+static_assert(kSegmentTiles > 0, "extra tiles are also the mark that tiles count their units");
 
 // CTAs of a grid at most: what the partials are sized for.
 constexpr int kMaxCtas = 148 * 3;
