@@ -329,7 +329,8 @@ cudaError_t run(const dhsa_rope_table& rope, const RopeArgs& a, cudaStream_t str
                            (PAGED ? (a.v.heads + C::kChunk - 1) / C::kChunk : 0);
   const long long blocks = (a.tokens * chunks + C::kUnits - 1) / C::kUnits;
   if (blocks * C::kUnits > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_early(rope_kernel<T, D, VEC, HEADS, PAGED>, static_cast<unsigned>(blocks), kThreads, 0, stream, rope, a);
+  return launch_early(rope_kernel<T, D, VEC, HEADS, PAGED>, static_cast<unsigned>(blocks), kThreads, 0, stream, rope,
+                      a);
 }
 
 // W: numbers of a 16-byte vector.
