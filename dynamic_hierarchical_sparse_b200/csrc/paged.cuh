@@ -25,6 +25,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The base that a row's weights 2^(x - base) are taken against, by its largest
+// logit so far (scores times scale, in log2 units): the largest weight becomes
+// 2^lift, so that those far below it keep their bits in f16, where numbers are
+// normal from 2^-14 and come in steps of 2^-24 below.  A weight is off by 2^-11 of
+// itself, or by 2^-(25 + lift) of the row's largest where that is more.  The sums of
+// weights carry the same factor.  Rounded up, so that x - base never passes lift.
+__device__ __forceinline__ float weight_base(float top_score, float scale_log2, float lift) {
+  return __fadd_ru(__fmul_ru(top_score, scale_log2), -lift);
+}
+constexpr float kTopLog2 = 15.f;  // f16 weights are 2^15 at most
+
 // One item: the query tokens [t0, t1) over the keys [lo, hi) of a table row.
 struct PagedItem {
   int t0, t1, lo, hi, row;

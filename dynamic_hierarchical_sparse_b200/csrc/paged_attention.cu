@@ -437,7 +437,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
         for (int e = 0; e < 2; ++e) {
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-          mnew[e] = fmaxf(m[e], mx[e] * scale_log2);
+          mnew[e] = fmaxf(m[e], weight_base(mx[e], scale_log2, kTopLog2));
           grew |= mnew[e] > m[e];
         }
         if (__any_sync(0xffffffffu, grew)) {
@@ -932,8 +932,12 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 #pragma unroll
   for (int c = 0; c < kCols; c += 2)
     store2(out + lane * kCols + c, acc[c] * inv, acc[c + 1] * inv);
-  if (w.lse != nullptr && lane == 0)
-    w.lse[static_cast<long long>(t) * w.num_q_heads + h] = limit > 0 ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  if (w.lse != nullptr && lane == 0) {
+    // (f16 weights are lifted by up to 2^15: taken out of both, the logarithm is of a number near the plain sum)
+    constexpr float kLift = sizeof(T) == 2 ? kTopLog2 : 0.f, kDown = sizeof(T) == 2 ? 0x1p-15f : 1.f;
+    w.lse[static_cast<long long>(t) * w.num_q_heads + h] =
+        limit > 0 ? ((m + kLift) + log2f(sum * kDown)) * kLn2 : -INFINITY;
+  }
 }
 
 int sm_count() {

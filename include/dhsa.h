@@ -502,8 +502,8 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * One token a sequence is a decode step; several are drafted tokens, or a
  * prompt's next part.  A group's prefix is read once for all its sequences.
  * L <= 0: out is 0 and lse -infinity.  scale <= 0 selects 1 / sqrt(d).  fp32
- * accumulation and softmax; bf16 problems take the weights in f16 (as
- * dhsa_attention).  A NaN or an infinity in a stored value (V) at a position
+ * accumulation and softmax; bf16 problems take the weights in f16, each off by
+ * 2^-11 of itself, or by 2^-36 of the row's largest where that is more.  A NaN or an infinity in a stored value (V) at a position
  * below a sequence's kv_lens, or in a shared prefix, may reach all the query
  * rows that are worked on together, also those to which the position is not
  * visible; keys (K), and slots at or behind kv_lens, reach no row that does not
