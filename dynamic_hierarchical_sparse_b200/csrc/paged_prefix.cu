@@ -227,8 +227,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           const int page_next = page_at(kt + 1);
           const unsigned bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
           const int in_page = ((walk.first + walk.kt + kt) * kBN + pp * box) & (ps - 1);
-          if (round > 0) ok = mbar_wait(bar(free + slot), (round - 1) & 1, abort_flag, w.status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (round > 0 && !(ok = mbar_wait_warp(bar(free + slot), (round - 1) & 1, abort_flag, w.status))) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), bytes);
           __syncwarp();
           if (page >= 0) tma_load_4d(dst0 + slot * C::kTile, map, bar(full + slot), sl * 64, in_page, h, page);
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int k0 = (first + kt) * kBN, pb = p_bar(a, mine);
         const uint32_t tS = tS0 + kBN * pb;
         if (!rehearsal) {
-          if (!(ok = mbar_wait(bar(kBarSFull + pb), p_phase(mine), abort_flag, w.status))) break;
+          if (!(ok = mbar_wait_warp(bar(kBarSFull + pb), p_phase(mine), abort_flag, w.status))) break;
           ++mine;
           tc_fence_after();
           if (k0 + kBN > hi) {
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             // NaN is NaN: V's rows there are zeroed (a thread a row; lanes that share
             // the tile write the same zeros)
             const int n = n0 + kt, s = n % C::kVStages;
-            if (!(ok = mbar_wait(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag, w.status))) break;
+            if (!(ok = mbar_wait_warp(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag, w.status))) break;
             if (row < kBN && k0 + row >= hi) {
 #pragma unroll 1
               for (int c = 0; c < D / 8; ++c)
@@ -528,7 +527,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           // done, since this S was issued after them (with one lane: waited for)
           if (C::kLanes == 1 && !rehearsal) {
             const int n = n0 + kt - 1;
-            if (!(ok = mbar_wait(bar(kBarVFree + n % C::kVStages), (n / C::kVStages) & 1, abort_flag, w.status))) break;
+            ok = mbar_wait_warp(bar(kBarVFree + n % C::kVStages), (n / C::kVStages) & 1, abort_flag, w.status);
+            if (!ok) break;
             tc_fence_after();
           }
           const uint64_t alpha2 = f2_pack(alpha, alpha);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       const bool more = walk.next();
       if (more) send_q(walk);
       if (some) {
-        if (!(ok = mbar_wait(bar(kBarODone + a), done[a] & 1, abort_flag, w.status))) break;
+        if (!(ok = mbar_wait_warp(bar(kBarODone + a), done[a] & 1, abort_flag, w.status))) break;
         tc_fence_after();
       }
       if (!ap) {
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarCross + a));
-        if (!(ok = mbar_wait(bar(kBarCross + 1 - a), joins & 1, abort_flag, w.status))) break;
+        if (!(ok = mbar_wait_warp(bar(kBarCross + 1 - a), joins & 1, abort_flag, w.status))) break;
         tc_fence_after();
         if (warp_valid) {
           uint32_t xm, xl;
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // no product of the next piece starts before both lanes have read TMEM
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPiece));
-        if (!(ok = mbar_wait(bar(kBarPiece), (done[0]) & 1, abort_flag, w.status))) break;
+        if (!(ok = mbar_wait_warp(bar(kBarPiece), (done[0]) & 1, abort_flag, w.status))) break;
       } else {
         if (!more) break;
       }
@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       if (!ap || count > 1) ++done[1];
       n0 += count;
     } while (true);
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (a Q sent for and not landed, where a wait gave up)
   }
 
   tc_fence_before();
