@@ -23,6 +23,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// Waits of these kernels are on their own CTA's warps and copies.  One that runs out
+// is reported, ends its CTA's work and no other's, and nothing of it is kept: the status
+// word gathers reports across calls, so no wait looks there (mbar_wait<false>).
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The base that a row's weights 2^(x - base) are taken against, by its largest

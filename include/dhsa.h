@@ -352,7 +352,9 @@ DHSA_API dhsa_status dhsa_plan_noalloc(const void* q, const void* k, const dhsa_
  * The status word of these calls is not cleared by them: it gathers the
  * reports of every call since the caller last zeroed the first 256 bytes of
  * the workspace (once, before the first call), so that a captured decode loop
- * can be checked after many steps.  dhsa_workspace_status reads it. */
+ * can be checked after many steps.  dhsa_workspace_status reads it.  A report
+ * stands for the calls that made it: later calls with the same workspace do not
+ * go by it, and their results are whole (DHSA_ERR_TIMEOUT included). */
 
 /* A packed [T, H, d] tensor whose tokens may lie apart (a slice of a fused
  * projection's output): the H * d elements of one token are contiguous, token

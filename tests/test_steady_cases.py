@@ -110,3 +110,20 @@ def test_many_tiles(name):
     assert torch.all(out[rows:] == 5.0) and torch.all(lse[rows:] == 5.0)
     first = out.clone()
     assert torch.equal(att(q, out), first)  # the same bits again
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["pieces_d128", "long_d256", "own_64", "f32_d128"])
+def test_an_earlier_report_does_not_end_a_call(name):
+    """The status word gathers reports; a timeout that an earlier call left there changes no later result."""
+    st = T.build(name)
+    cache, batch, q = st.cache(), st.batch(), st.q.cuda()
+    att = api.PagedAttention(cache, batch, st.hq)
+    want = att(q, torch.zeros_like(q))[:st.cu[-1]].clone()
+    assert att.status() == 0
+    att.ws[:4].view(torch.int32).fill_(1)  # as a wait that ran out would leave it
+    att.ws[256:].fill_(0xFF)
+    got = att(q, torch.zeros_like(q))[:st.cu[-1]]
+    assert torch.equal(got, want) and att.status() == 5
+    att.reset()
+    assert att.status() == 0

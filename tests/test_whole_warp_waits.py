@@ -32,7 +32,7 @@ def test_waits(name):
     lines = _lines(name)
     warp = 0
     for i, line in enumerate(lines):
-        if "mbar_wait_warp(" in line:
+        if re.search(r"\bmbar_wait_warp\b", line):
             warp += 1
             assert not any("lane == 0" in c for c in _branch(lines, i)), line
         if re.search(r"\bmbar_wait(?:_spin)?(?:<\w+>)?\(", line):
@@ -40,6 +40,17 @@ def test_waits(name):
             dropped = "&never" in line
             assert lone or dropped, (i + 1, line)
     assert warp >= 3
+
+
+@pytest.mark.parametrize("name", ["paged_attention.cu", "paged_prefix.cu"])
+def test_no_wait_goes_by_an_earlier_calls_report(name):
+    """The status word of these calls is not cleared by them, so no wait may end by what it says."""
+    for line in _lines(name):
+        for wait in re.findall(r"\bmbar_wait\w*(?:<\w+>)?\(", line):
+            assert wait.endswith("<false>("), line
+    text = open(os.path.join(CSRC, "common.cuh")).read()
+    reads = re.findall(r"if \((.*)reinterpret_cast<volatile uint32_t\*>\(status\)", text)
+    assert len(reads) == 2 and all(r.startswith("kHeed && ") for r in reads)
 
 
 def test_the_warp_wait_votes():
