@@ -337,6 +337,9 @@ struct PagedWalk {
   __device__ __forceinline__ int seg() const { return h * rt + ri; }
   __device__ __forceinline__ int row0() const { return ri << ts; }  // the tile's first row
   __device__ __forceinline__ int rows() const { return (it.t1 - it.t0) * group_heads; }
+  // the piece's keys
+  __device__ __forceinline__ int key_begin() const { return max((first + kt) * BN, it.lo); }
+  __device__ __forceinline__ int key_end() const { return min((first + kt + count) * BN, it.hi); }
   // false: no work for this CTA
   __device__ __forceinline__ bool init(const PagedArgs* args, int gh, const PagedList& list, const PagedScan* sc) {
     p = args;
@@ -389,5 +392,137 @@ struct PagedWalk {
     return true;
   }
 };
+
+// ---------------------------------------------------------- rows once more
+// The kernels take rows together, so a value that a row does not see, or that its
+// products cannot take, can still reach its sums: a weight of 0 times a NaN or an
+// infinity in V is NaN, and in fp32 the parts of an infinity (or of a number that
+// rounds to one) cancel to NaN.  A partial that came out so is made again for its row
+// alone, in plain fp32 products over the keys that the row sees.  Never on the way of
+// finite data; a warp takes about 60 ns a key.
+
+// N consecutive numbers as fp32.
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float (&x)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p + c);
+    x[c] = v.x;
+    x[c + 1] = v.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + c));
+    x[c] = v.x;
+    x[c + 1] = v.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_row(const __half* p, float (&x)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(p + c));
+    x[c] = v.x;
+    x[c + 1] = v.y;
+  }
+}
+
+template <int D>
+struct RowAgain {
+  float m, l, o[D / 32];  // m: largest logit (log2 units); o: columns lane * D / 32 and on
+};
+
+// Query row `q` (its head's first number) over the keys [k0, k1) of a table row and
+// KV head, by one warp: a lane takes the logit of a key, then its columns of O.
+template <int D, typename T, typename TV>
+__device__ __noinline__ RowAgain<D> paged_row_again(const PagedWork& w, int table_row, int h, const T* q, int k0,
+                                                    int k1) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float scale_log2 = w.scale * kLog2e;
+  RowAgain<D> r;
+  r.m = -INFINITY;
+  r.l = 0.f;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) r.o[c] = 0.f;
+  const int* table = w.p.block_table + static_cast<long long>(table_row) * w.p.table_stride;
+#pragma unroll 1
+  for (int kb = k0; kb < k1; kb += 32) {
+    const int key = kb + lane, n = min(k1 - kb, 32);
+    const int pg = lane < n ? table[key >> w.p.page_shift] : -1;
+    long long at = -1;  // the key's first number in the pages; a page outside the cache reads as zeros
+    if (static_cast<unsigned>(pg) < static_cast<unsigned>(w.p.num_pages))
+      at = pg * w.p.page_stride + (static_cast<long long>(h) * w.p.page_size + (key & (w.p.page_size - 1))) * D;
+    float dot = 0.f;
+    if (at >= 0) {
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        float a[4], b[4];
+        load_row(q + c, a);
+        load_row(static_cast<const T*>(w.p.k_pages) + at + c, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = fmaf(a[e], b[e], dot);
+      }
+    }
+    const float x = lane < n ? dot * scale_log2 : -INFINITY;
+    float top = fmaxf(r.m, x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float base = top == -INFINITY ? 0.f : top;
+    const float f = ex2_approx(r.m - base), p = ex2_approx(x - base);
+    float sum = p;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    r.m = top;
+    r.l = fmaf(r.l, f, sum);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) r.o[c] *= f;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const long long v_at = __shfl_sync(0xffffffffu, at, j);
+      const float pj = __shfl_sync(0xffffffffu, p, j);
+      float v[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[c] = 0.f;
+      if (v_at >= 0) load_row(static_cast<const TV*>(w.p.v_pages) + v_at + lane * kCols, v);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) r.o[c] = fmaf(pj, v[c], r.o[c]);
+    }
+  }
+  return r;
+}
+
+// Whether a number is an infinity or NaN, for sums of such marks: 0, or NaN.
+__device__ __forceinline__ float odd_mark(float x, float sum) { return fmaf(x, 0.f, sum); }
+
+// The rows of a piece whose partials in `list` are not finite, by four warps: segment
+// of KV head h and first row row0 of item i, `valid` rows, keys [k0, k1) of it, partial
+// rows from `part` on.  kAll: every such row, else those that do not see all the keys.
+template <int D, typename T, typename TV, bool kAll>
+__device__ __noinline__ void paged_rows_again(const PagedWork& w, const PagedList& list, const PagedItem it, int i,
+                                              int h, int row0, int valid, int k0, int k1, int part) {
+  constexpr int kCols = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gh = w.by_group.d;
+#pragma unroll 1
+  for (int x = warp; x < valid; x += 4) {
+    float* o = list.part_o + static_cast<long long>(part + x) * D + lane * kCols;
+    float mark = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) mark = odd_mark(o[c], mark);
+    const int r = row0 + x, tr = w.by_group(r), t = it.t0 + tr;
+    const int b = i < w.p.num_groups ? paged_seq_of(w.p, t) : it.row;
+    const int lim = paged_limit(w.p, b, t);
+    if (!__any_sync(0xffffffffu, mark != 0.f) || lim <= 0 || (!kAll && lim >= k1)) continue;
+    const T* q = static_cast<const T*>(w.q) + t * w.q_stride + static_cast<long long>((h - tr) * gh + r) * D;
+    const RowAgain<D> a = paged_row_again<D, T, TV>(w, it.row, h, q, k0, min(lim, k1));
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[c] = a.o[c];
+    if (lane == 0) list.part_ml[part + x] = make_float2(a.m, a.l);
+  }
+}
 
 }  // namespace dhsa

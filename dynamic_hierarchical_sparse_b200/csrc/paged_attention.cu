@@ -200,7 +200,31 @@ __device__ __forceinline__ bool compute_sync_or(bool x) {
 // fp32 12.7 -> 12.3 (a call that has both kinds, 4 answers to 2500 tokens, 13.7 ->
 // 13.9: more code to fetch).
 constexpr int kFew = 4;
-template <int D, typename C, int kMax, int WM, int WN, typename Walk>
+
+// Storage types of the pages, and which partials are made again (see paged_rows_again).
+struct Bf16Pages {
+  using K = __nv_bfloat16;
+  using V = __half;
+  static constexpr bool kAll = false;
+};
+struct F32Pages {
+  using K = float;
+  using V = float;
+  static constexpr bool kAll = true;
+};
+
+// The end of a piece: false if a warp's wait gave up; `odd`: this thread met a number
+// of the piece's partials that is not finite.  One barrier where neither is so.
+template <int D, typename P, typename Walk>
+__device__ __forceinline__ bool close_piece(const PagedWork& w, const Walk& k, int valid, int part, bool ok, bool odd) {
+  if (!compute_sync_or<128>(!ok || odd)) return true;
+  if (compute_sync_or<128>(!ok)) return false;
+  paged_rows_again<D, typename P::K, typename P::V, P::kAll>(w, w.list, k.it, k.i, k.h, k.row0(), valid, k.key_begin(),
+                                                             k.key_end(), part);
+  return true;
+}
+
+template <int D, typename C, typename P, int kMax, int WM, int WN, typename Walk>
 __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, const Ring& ctx, float (&o)[D / 8][4],
                                              const float (&m)[2], float (&l)[2], bool ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wm = warp / WN;
@@ -208,6 +232,7 @@ __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, 
   float2* ml = reinterpret_cast<float2*>(ctx.smem + C::kOffMl);
   const int part = paged_part_row(blockIdx.x, kMax, k.item_row, k.seg(), k.ts);
   const int valid = min(k.rows() - k.row0(), WM * 16);
+  float mark = 0.f;
   if constexpr (kMax == 16) {
     if (valid <= kFew) {
       constexpr int kStride = D + 8;  // floats; four rows' writes hit all banks
@@ -238,10 +263,11 @@ __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, 
           a.z = fmaf(u.z, f, a.z);
           a.w = fmaf(u.w, f, a.w);
         }
+        mark = odd_mark(a.w, odd_mark(a.z, odd_mark(a.y, odd_mark(a.x, mark))));
         *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + 4 * v) = a;
         if (v == 0) w.list.part_ml[part + r] = make_float2(top, sum);
       }
-      return !compute_sync_or<128>(!ok);
+      return close_piece<D, P>(w, k, valid, part, ok, mark != 0.f);
     }
   }
 #pragma unroll
@@ -294,35 +320,40 @@ __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, 
         a.z += u.z;
         a.w += u.w;
       }
+      mark = odd_mark(a.w, odd_mark(a.z, odd_mark(a.y, odd_mark(a.x, mark))));
       *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + c * (D / 4) + 4 * v) = a;
     }
     if (c < 3) compute_sync<128>();
   }
-  return !compute_sync_or<128>(!ok);
+  return close_piece<D, P>(w, k, valid, part, ok, mark != 0.f);
 }
 
 // The same where every warp has 16 rows of its own: the fragments go out as they
 // are, a row's 32-byte sector from four lanes (16 answers to 1000 tokens of d 256
 // 29.9 -> 29.0 us, 4 of 4 tokens of d 64 to 2567 16.0 -> 15.4, against the way above).
-template <int D, int kMax, typename Walk>
+template <int D, typename P, int kMax, typename Walk>
 __device__ __forceinline__ bool finish_apart(const PagedWork& w, const Walk& k, const float (&o)[D / 8][4],
                                              const float (&m)[2], float (&l)[2], bool ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = paged_part_row(blockIdx.x, kMax, k.item_row, k.seg(), k.ts);
+  const int valid = k.rows() - k.row0();
+  float mark = 0.f;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     const int r = warp * 16 + (lane >> 2) + 8 * e;
-    if (r < k.rows() - k.row0()) {
+    if (r < valid) {
       if ((lane & 3) == 0) w.list.part_ml[part + r] = make_float2(m[e], l[e]);
       float* dst = w.list.part_o + static_cast<long long>(part + r) * D + 2 * (lane & 3);
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
+      for (int j = 0; j < D / 8; ++j) {
+        mark = odd_mark(o[j][2 * e + 1], odd_mark(o[j][2 * e], mark));
         *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
+      }
     }
   }
-  return !compute_sync_or<128>(!ok);
+  return close_piece<D, P>(w, k, min(valid, 64), part, ok, mark != 0.f);
 }
 
 // One piece on the four compute warps: WM warps along the rows, WN along a
@@ -500,9 +531,9 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
   }
 
   if constexpr (WN == 1) {
-    return finish_apart<D, kMax>(w, k, o, m, l, ok);
+    return finish_apart<D, Bf16Pages, kMax>(w, k, o, m, l, ok);
   } else {
-    return finish_piece<D, C, kMax, WM, WN>(w, k, ctx, o, m, l, ok);
+    return finish_piece<D, C, Bf16Pages, kMax, WM, WN>(w, k, ctx, o, m, l, ok);
   }
 }
 
@@ -576,8 +607,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 // it has them all: h + l is x to 2^-23, and a b = h h' + h l' + l h' to about 2^-21
 // of |a b|, accumulated in fp32.  The split takes integer instructions, which takes
 // 4 sequences on 14117 keys from 74 to 64 us with d 256 and from 42 to 38 with d
-// 128 against the conversion's own; an infinity has a NaN for l, and a NaN whose
-// bits the rounding carries past the sign leaves itself in l.  (The same in FFMA is
+// 128 against the conversion's own; an infinity, and a
+// number that rounds to one, has no l that adds up to it (its products cancel to NaN, and
+// the row is made again, see paged_rows_again), and a NaN whose bits the rounding carries
+// past the sign leaves itself in l.  (The same in FFMA is
 // bound by shared memory: 16 rows are too few for a register block that would feed
 // it.)  A tile is 16 rows and 32 keys; the four warps split the keys.
 constexpr int kFBN = 32;    // keys a tile
@@ -761,7 +794,7 @@ __device__ __forceinline__ bool f32_piece(const PagedWork& w, const PagedWalk<kF
     if (lane == 0) mbar_arrive(bar_empty<C::kStages>(ctx, ctx.stage));
     ctx.template next<C::kStages>();
   }
-  return finish_piece<D, C, kFRows, 1, 4>(w, k, ctx, o, m, l, ok);
+  return finish_piece<D, C, F32Pages, kFRows, 1, 4>(w, k, ctx, o, m, l, ok);
 }
 
 template <int D>

@@ -81,6 +81,42 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// A warp's rows (a lane each) marked `mine`, where the `cols` columns of their partial
+// at dst, from col0 on, are not finite: made again for the keys [k0, k1) that each sees,
+// against the base that the row's stored sum has.
+template <int D>
+__device__ __noinline__ void short_rows_again(const PagedWork& w, bool mine, const __nv_bfloat16* q, float* dst,
+                                              int col0, int cols, float base, int table_row, int h, int k0, int k1) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x & 31;
+  const bool own = lane * kCols >= col0 && lane * kCols < col0 + cols;
+  __syncwarp();  // the rows' stores, read and written here by other lanes
+  uint32_t rows = __ballot_sync(0xffffffffu, mine);
+#pragma unroll 1
+  for (; rows != 0u; rows &= rows - 1u) {
+    const int src = __ffs(rows) - 1;
+    float* o = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), src)) +
+               lane * kCols;
+    const auto* q_row = reinterpret_cast<const __nv_bfloat16*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q), src));
+    const int end = __shfl_sync(0xffffffffu, k1, src);
+    const float to = __shfl_sync(0xffffffffu, base, src);
+    float mark = 0.f;
+    if (own) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) mark = odd_mark(o[c], mark);
+    }
+    if (!__any_sync(0xffffffffu, mark != 0.f)) continue;
+    const RowAgain<D> r = paged_row_again<D, __nv_bfloat16, __half>(w, table_row, h, q_row, k0, end);
+    const float f = to == -INFINITY ? 0.f : ex2_approx(r.m - to);
+    if (own) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) o[c] = r.o[c] * f;
+    }
+  }
+  __syncwarp();
+}
+
 enum {
   kBarKFull = 0,    // + stage
   kBarVFull = 4,    // + stage
@@ -582,6 +618,16 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       }
       const int part = paged_part_row(blockIdx.x, C::kRows, walk.item_row, walk.seg(), walk.ts) + in_tile;
       float* dst = w.prefix.part_o + static_cast<long long>(part) * D;
+      // rows that do not see all of the piece's keys may have met values that are not theirs: what
+      // making them again takes (see paged_rows_again)
+      const int key_begin = walk.key_begin(), key_end = walk.key_end(), table_row = walk.it.row, head = walk.h;
+      const bool short_row = valid && lim > 0 && lim < key_end;
+      const __nv_bfloat16* q_row = nullptr;
+      if (short_row) {
+        const int r = walk.row0() + in_tile, tr = w.by_group(r);
+        q_row = static_cast<const __nv_bfloat16*>(w.q) + (walk.it.t0 + tr) * w.q_stride +
+                static_cast<long long>((head - tr) * gh + r) * D;
+      }
       const bool some = kt0 < count;  // lanes apart: lane 1 has no tile in a piece of one
       const bool more = walk.next();
       if (more) send_q(walk);
@@ -603,6 +649,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
               for (int e = 0; e < 32; e += 8) store_row8(dst + 32 * c + e, o + e);
             }
           }
+          if (__any_sync(0xffffffffu, short_row))
+            short_rows_again<D>(w, short_row, q_row, dst, 0, D, m_run, table_row, head, key_begin, min(lim, key_end));
           tc_fence_before();  // the next piece's P V overwrites O after this warp's next arrival
         }
       } else {
@@ -645,6 +693,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
               for (int e = 0; e < 32; e += 8) store_row8(dst + a * kHalf + 32 * c + e, o0 + e);
             }
           }
+          if (__any_sync(0xffffffffu, short_row))
+            short_rows_again<D>(w, short_row, q_row, dst, a * kHalf, kHalf, top, table_row, head, key_begin,
+                                min(lim, key_end));
           tc_fence_before();
         }
         ++joins;

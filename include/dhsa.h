@@ -505,13 +505,12 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * prompt's next part.  A group's prefix is read once for all its sequences.
  * L <= 0: out is 0 and lse -infinity.  scale <= 0 selects 1 / sqrt(d).  fp32
  * accumulation and softmax; bf16 problems take the weights in f16, each off by
- * 2^-11 of itself, or by 2^-36 of the row's largest where that is more.  A NaN or an infinity in a stored value (V) at a position
- * below a sequence's kv_lens, or in a shared prefix, may reach all the query
- * rows that are worked on together, also those to which the position is not
- * visible; keys (K), and slots at or behind kv_lens, reach no row that does not
- * see them.  An infinity in a query or a visible key of an fp32 problem makes
- * the row NaN (its products are taken in two parts, see paged_attention.cu); in
- * bf16 it is an infinite score, as in plain arithmetic.  Results are the same from call to call.  A batch whose tables
+ * 2^-11 of itself, or by 2^-36 of the row's largest where that is more.  Values
+ * and keys that a row does not see (of later tokens, of a shared prefix behind its
+ * sequence's end, of slots not written yet) change nothing in it, whatever they
+ * hold; infinities and NaN that it sees count as in plain arithmetic (a logit of
+ * -infinity has no weight, one of +infinity makes the row NaN).  Rows that meet some
+ * not finite are slow.  Results are the same from call to call.  A batch whose tables
  * leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
  * 32 keys is refused as DHSA_ERR_UNSUPPORTED.
  *   q, out     [T, Hq, d] in the cache's dtype; must not overlap
