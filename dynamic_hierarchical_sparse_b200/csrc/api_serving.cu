@@ -4,6 +4,9 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <cmath>
+#include <limits>
+
 #include "serving.h"
 
 namespace dhsa {
@@ -11,7 +14,6 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr size_t kStatusBytes = 256;
-constexpr double kPi = 3.14159265358979323846;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -148,21 +150,29 @@ dhsa_status attention_layout(const dhsa_paged_cache* c, const dhsa_paged_batch* 
   return DHSA_OK;
 }
 
-// The frequencies (radians a position) as fractions of a turn.
-dhsa_status fill_turns(dhsa_rope_table* rope, int32_t rotary_dim, int32_t interleaved, const double* freq,
+// Frequencies are worked out in 64 bits of mantissa, one more than a fraction of a
+// turn keeps: in a double's 53 they would be off by up to 2^-55 turns a position,
+// 2^-24 turns at the far end of the positions.
+using Freq = long double;
+static_assert(std::numeric_limits<Freq>::digits >= 64, "the fractions of a turn have 64 bits");
+constexpr Freq kPi = 3.14159265358979323846264338327950288L;
+
+// The frequencies (radians a position) as fractions of a turn, rounded to 64 bits.
+dhsa_status fill_turns(dhsa_rope_table* rope, int32_t rotary_dim, int32_t interleaved, const Freq* freq,
                        double factor) {
   if (!isfinite(factor) || !isfinite(static_cast<float>(factor))) return DHSA_ERR_INVALID_ARG;
   for (int i = 0; i < rotary_dim / 2; ++i)
-    if (!isfinite(freq[i])) return DHSA_ERR_INVALID_ARG;
+    if (!std::isfinite(freq[i])) return DHSA_ERR_INVALID_ARG;
   rope->rotary_dim = rotary_dim;
   rope->interleaved = interleaved != 0;
   rope->factor = static_cast<float>(factor);
   for (int i = 0; i < DHSA_ROPE_MAX_PAIRS; ++i) {
     rope->turns[i] = 0;
     if (i >= rotary_dim / 2) continue;
-    double turn = freq[i] / (2 * kPi);
-    turn -= floor(turn);  // [0, 1]: 1 only by rounding
-    rope->turns[i] = turn >= 1.0 ? 0 : static_cast<uint64_t>(ldexp(turn, 64));
+    Freq turn = freq[i] / (2 * kPi);
+    turn -= std::floor(turn);
+    turn = std::round(std::ldexp(turn, 64));  // 2^64, a whole turn, is none
+    rope->turns[i] = turn >= std::ldexp(Freq(1), 64) ? 0 : static_cast<uint64_t>(turn);
   }
   return DHSA_OK;
 }
@@ -178,7 +188,9 @@ dhsa_status dhsa_rope_init_freq(dhsa_rope_table* rope, int32_t rotary_dim, int32
                                 const double* inv_freq, double factor) {
   if (rope == nullptr || inv_freq == nullptr) return DHSA_ERR_INVALID_ARG;
   if (rotary_dim < 2 || rotary_dim > 2 * DHSA_ROPE_MAX_PAIRS || rotary_dim % 2 != 0) return DHSA_ERR_INVALID_ARG;
-  return fill_turns(rope, rotary_dim, interleaved, inv_freq, factor);
+  Freq freq[DHSA_ROPE_MAX_PAIRS];
+  for (int i = 0; i < rotary_dim / 2; ++i) freq[i] = inv_freq[i];
+  return fill_turns(rope, rotary_dim, interleaved, freq, factor);
 }
 
 dhsa_status dhsa_rope_init(dhsa_rope_table* rope, int32_t rotary_dim, int32_t interleaved, double base,
@@ -197,31 +209,31 @@ dhsa_status dhsa_rope_init(dhsa_rope_table* rope, int32_t rotary_dim, int32_t in
   if (kind == DHSA_ROPE_YARN &&
       !(sc->beta_slow > 0 && sc->beta_fast >= sc->beta_slow && isfinite(sc->beta_fast)))
     return DHSA_ERR_INVALID_ARG;
-  double freq[DHSA_ROPE_MAX_PAIRS];
+  Freq freq[DHSA_ROPE_MAX_PAIRS];
   double factor = 1.0, low = 0, high = 0;
   if (kind == DHSA_ROPE_YARN) {
     // the pair index that makes `turns` turns in the original length
     auto index = [&](double turns) {
-      return rotary_dim * log(sc->original_len / (turns * 2 * kPi)) / (2 * log(base));
+      return rotary_dim * log(sc->original_len / (turns * 2 * static_cast<double>(kPi))) / (2 * log(base));
     };
     low = fmax(floor(index(sc->beta_fast)), 0.0);
     high = fmin(ceil(index(sc->beta_slow)), rotary_dim - 1.0);
     if (high == low) high += 0.001;
     factor = 0.1 * log(sc->factor) + 1.0;
   }
+  const Freq one = 1, zero = 0, by = kind == DHSA_ROPE_UNSCALED ? 1.0 : sc->factor;
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    const double f = pow(base, -2.0 * i / rotary_dim);
-    double y = f;
+    const Freq f = std::pow(static_cast<Freq>(base), -2 * static_cast<Freq>(i) / rotary_dim);
+    Freq y = f;
     if (kind == DHSA_ROPE_LINEAR) {
-      y = f / sc->factor;
+      y = f / by;
     } else if (kind == DHSA_ROPE_LLAMA3) {
-      const double turns = sc->original_len * f / (2 * kPi);
-      const double mix = (turns - sc->low_freq_factor) / (sc->high_freq_factor - sc->low_freq_factor);
-      const double keep = fmin(fmax(mix, 0.0), 1.0);
-      y = keep * f + (1 - keep) * (f / sc->factor);
+      const Freq turns = sc->original_len * f / (2 * kPi), lo = sc->low_freq_factor, hi = sc->high_freq_factor;
+      const Freq keep = std::fmin(std::fmax((turns - lo) / (hi - lo), zero), one);
+      y = keep * f + (1 - keep) * (f / by);
     } else if (kind == DHSA_ROPE_YARN) {
-      const double share = fmin(fmax((i - low) / (high - low), 0.0), 1.0);
-      y = share * (f / sc->factor) + (1 - share) * f;
+      const Freq share = std::fmin(std::fmax((i - static_cast<Freq>(low)) / (static_cast<Freq>(high) - low), zero), one);
+      y = share * (f / by) + (1 - share) * f;
     }
     freq[i] = y;
   }

@@ -3,8 +3,8 @@
 // slot, Q rotated beside them), in one launch each.
 //
 // Pair i of a token at position p turns by p * f_i.  f_i / (2 pi) comes as a
-// 64-bit binary fraction of a turn, so p times it modulo 2^64 is the exact
-// phase of any position; the top 32 bits are split into the nearest quarter
+// 64-bit binary fraction of a turn, so p times it modulo 2^64 is the phase of
+// any position (to |p| 2^-63 turns); the top 32 bits are split into the nearest quarter
 // turn and a remainder of at most an eighth of a turn, whose sine and cosine
 // are taken in fp32 (no loss at far positions, where an fp32 product p * f_i
 // would be off by p * 2^-24 radians).

@@ -381,10 +381,10 @@ typedef struct {
  *           between the pair indexes that make beta_fast and beta_slow turns in
  *           original_len (rounded down and up, kept within 0 .. rotary_dim - 1),
  *           and a = 0.1 ln(factor) + 1; otherwise a = 1.
- * Angles are exact for every position: the table holds f_i / (2 pi) as a
- * 64-bit binary fraction of a turn, and position times fraction is integer
- * arithmetic modulo one turn (error 2^-32 turns from the top 32 bits, plus
- * |p| 2^-64).  cos, sin and the rotation are fp32, each output rounded once. */
+ * The table holds f_i / (2 pi) as a 64-bit binary fraction of a turn, rounded, and
+ * position times fraction is integer arithmetic modulo one turn, so angles stay right
+ * at every position: within 2^-32 turns from taking the top 32 bits, plus |p| 2^-63
+ * for frequencies up to 1 (2^-64 (1/2 + |f_i|) |p| for given ones).  cos, sin and the rotation are fp32, each output rounded once. */
 #define DHSA_ROPE_MAX_PAIRS 128
 typedef enum {
   DHSA_ROPE_UNSCALED = 0,
