@@ -263,11 +263,11 @@ __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, 
           a.z = fmaf(u.z, f, a.z);
           a.w = fmaf(u.w, f, a.w);
         }
-        mark = odd_mark(a.w, odd_mark(a.z, odd_mark(a.y, odd_mark(a.x, mark))));
+        mark = odd_mark(a.x, a.y, odd_mark(a.z, a.w, mark));
         *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + 4 * v) = a;
         if (v == 0) w.list.part_ml[part + r] = make_float2(top, sum);
       }
-      return close_piece<D, P>(w, k, valid, part, ok, mark != 0.f);
+      return close_piece<D, P>(w, k, valid, part, ok, is_odd(mark));
     }
   }
 #pragma unroll
@@ -320,12 +320,12 @@ __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, 
         a.z += u.z;
         a.w += u.w;
       }
-      mark = odd_mark(a.w, odd_mark(a.z, odd_mark(a.y, odd_mark(a.x, mark))));
+      mark = odd_mark(a.x, a.y, odd_mark(a.z, a.w, mark));
       *reinterpret_cast<float4*>(w.list.part_o + static_cast<long long>(part + r) * D + c * (D / 4) + 4 * v) = a;
     }
     if (c < 3) compute_sync<128>();
   }
-  return close_piece<D, P>(w, k, valid, part, ok, mark != 0.f);
+  return close_piece<D, P>(w, k, valid, part, ok, is_odd(mark));
 }
 
 // The same where every warp has 16 rows of its own: the fragments go out as they
@@ -348,12 +348,12 @@ __device__ __forceinline__ bool finish_apart(const PagedWork& w, const Walk& k, 
       float* dst = w.list.part_o + static_cast<long long>(part + r) * D + 2 * (lane & 3);
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
-        mark = odd_mark(o[j][2 * e + 1], odd_mark(o[j][2 * e], mark));
+        mark = odd_mark(o[j][2 * e], o[j][2 * e + 1], mark);
         *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
       }
     }
   }
-  return close_piece<D, P>(w, k, min(valid, 64), part, ok, mark != 0.f);
+  return close_piece<D, P>(w, k, min(valid, 64), part, ok, is_odd(mark));
 }
 
 // One piece on the four compute warps: WM warps along the rows, WN along a

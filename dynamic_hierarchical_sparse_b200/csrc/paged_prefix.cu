@@ -104,15 +104,11 @@ __device__ __noinline__ void short_rows_again(const PagedWork& w, bool mine, con
     float mark = 0.f;
     if (own) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) mark = odd_mark(o[c], mark);
+      for (int c = 0; c < kCols; c += 2) mark = odd_mark(o[c], o[c + 1], mark);
     }
-    if (!__any_sync(0xffffffffu, mark != 0.f)) continue;
+    if (!__any_sync(0xffffffffu, is_odd(mark))) continue;
     const RowAgain<D> r = paged_row_again<D, __nv_bfloat16, __half>(w, table_row, h, q_row, k0, end);
-    const float f = to == -INFINITY ? 0.f : ex2_approx(r.m - to);
-    if (own) {
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) o[c] = r.o[c] * f;
-    }
+    if (own) put_again<D>(r, to, o);
   }
   __syncwarp();
 }
