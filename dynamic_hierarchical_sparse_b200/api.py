@@ -676,7 +676,8 @@ class PagedBatch:
 
     def __init__(self, cu_q, kv_lens: torch.Tensor, block_table: torch.Tensor, group_ptr=None,
                  prefix_lens: Optional[torch.Tensor] = None):
-        self.h_cu = np.ascontiguousarray(np.asarray(cu_q, dtype=np.int32))
+        # copies: the offsets on the host and on the device have to stay the same ones
+        self.h_cu = np.asarray(cu_q, dtype=np.int32).copy(order="C")
         if self.h_cu.ndim != 1 or self.h_cu.shape[0] < 1:
             raise ValueError("cu_q must have B + 1 entries")
         self.num_seqs = int(self.h_cu.shape[0] - 1)
@@ -696,7 +697,7 @@ class PagedBatch:
         self.d_cu = torch.from_numpy(self.h_cu).to(dev)
         groups, self.h_groups, self.d_groups = 0, None, None
         if group_ptr is not None:
-            self.h_groups = np.ascontiguousarray(np.asarray(group_ptr, dtype=np.int32))
+            self.h_groups = np.asarray(group_ptr, dtype=np.int32).copy(order="C")
             groups = int(self.h_groups.shape[0] - 1)
             if groups < 1:
                 raise ValueError("group_ptr must have G + 1 entries, G >= 1")
