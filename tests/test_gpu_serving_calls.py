@@ -28,3 +28,22 @@ def test_a_batch_keeps_its_own_offsets(make):
     q = st.q.cuda()
     got = api.PagedAttention(st.cache(), batch, 8)(q, torch.empty_like(q))
     assert torch.equal(got, api.PagedAttention(st.cache(), st.batch(), 8)(q, torch.empty_like(q)))
+
+
+@pytest.mark.parametrize("room", [0, 1 << 18])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_batches_without_work(dt, room):
+    """Every sequence idle, empty prefixes, prefixes behind idle sequences: zeros, lse of -infinity, nothing reported."""
+    for held, prefix in (([0] * 9, [0]), ([0] * 9, [40]), ([5] * 9, [0]), ([0] * 8 + [41], [40])):
+        st = C.Step(2, dt, 16, 2, 64, 16, [1] * 9, held, ([0, 9], prefix), room=room)
+        q, att = st.q.cuda(), api.PagedAttention(st.cache(), st.batch(), 16)
+        att.ws[256:].fill_(0xFF)
+        out, lse = torch.full_like(q, 3.0), torch.empty(9, 16, device="cuda")
+        att(q, out, lse=lse)
+        want, want_lse, mean = st.want()
+        bound, lse_bound = st.bounds(want, want_lse, mean)
+        assert att.status() == 0
+        assert np.all(np.abs(out.double().cpu().numpy() - want) <= bound)
+        idle = np.array(held) == 0
+        got = lse.double().cpu().numpy()
+        assert np.all(got[idle] == -np.inf) and np.all(np.abs(got[~idle] - want_lse[~idle]) <= lse_bound[~idle])
