@@ -56,6 +56,12 @@ CASES = {
                  dict(kind="list", pieces=2, tiles=10)),
     "f32_d64": (F32, 16, 4, 64, 64, ([9] * 5, [3001 + 511 * b for b in range(5)], None),
                 dict(kind="list", pieces=2, tiles=10)),
+    # contexts of 20 to 128 thousand tokens
+    "prefix_128k": (BF16, 16, 2, 128, 16, _drafted(1, 16, 1, 131072), dict(kind="prefix", pieces=1, tiles=10, apart=True)),
+    "prefix_128k_rows": (BF16, 32, 2, 128, 64, _drafted(1, 16, 1, 131059), dict(kind="prefix", pieces=1, tiles=10, apart=False)),
+    "prefix_40k_d256": (BF16, 16, 2, 256, 16, _drafted(1, 12, 1, 40001), dict(kind="prefix", pieces=1, tiles=8, apart=None)),
+    "own_60k": (BF16, 8, 2, 128, 128, ([1, 2, 1], [60001, 41007, 128], None), dict(kind="list", pieces=2, tiles=10)),
+    "f32_20k": (F32, 8, 2, 128, 16, _drafted(1, 6, 1, 20011), dict(kind="list", pieces=2, tiles=8)),
     "f32_d256_group": (F32, 8, 2, 256, 32, _drafted(1, 5, 3, 6000), dict(kind="list", pieces=2, tiles=10)),
 }
 

@@ -91,8 +91,11 @@ def test_definition_is_the_oracles():
             assert np.allclose(got, want, rtol=0, atol=1e-12)
 
 
+LONG = ["prefix_128k", "prefix_128k_rows", "prefix_40k_d256", "own_60k", "f32_20k"]
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("name", T.CASES)
+@pytest.mark.parametrize("name", [n for n in T.CASES if n not in LONG])
 def test_many_tiles(name):
     api.lib()
     st = T.build(name)
@@ -110,6 +113,38 @@ def test_many_tiles(name):
     assert torch.all(out[rows:] == 5.0) and torch.all(lse[rows:] == 5.0)
     first = out.clone()
     assert torch.equal(att(q, out), first)  # the same bits again
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", LONG + ["long_d128"])
+def test_long_contexts_closely(name):
+    """Long contexts within bounds that count the additions in a row: a piece's keys, then the partials, where
+    Step.bounds takes all keys; and f16's steps below its normal numbers, 2^-36 of the largest weight."""
+    dt, hq, hkv, d = T.CASES[name][:4]
+    st = T.build(name, seed=5)
+    st.v_pages += 1.0
+    q, rows = st.q.cuda(), st.cu[-1]
+    att = api.PagedAttention(st.cache(), st.batch(), st.hq)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    att(q, out, lse=lse)
+    assert att.status() == 0
+    want, want_lse, mean = T.want(st, "cuda")
+    fin = lambda t: np.nan_to_num(t.double().numpy(), nan=0.0)  # noqa: E731
+    qn = np.linalg.norm(fin(st.q[:rows]), axis=-1).reshape(rows, hkv, -1)
+    kn = np.linalg.norm(fin(st.k_pages), axis=-1).max(axis=(0, 2))
+    x = (qn * kn[:, None]).reshape(rows, hq) * d ** -0.5
+    chain = T.reached(name)[1] * 128 + T.SMS * 3
+    dx = (d + 4) * C.F32 * x + 3 * 2.0 ** -22 + chain * C.F32
+    f16 = dt == torch.bfloat16
+    err = (2 * dx + (2.0 ** -11 if f16 else 0.0))[..., None] * mean
+    err = err + (max(st.held) * 2.0 ** -36 * np.abs(fin(st.v_pages)).max() if f16 else 0.0)
+    bound = C.half_step(dt) * (np.abs(want) + err) + err
+    off = np.abs(out[:rows].double().cpu().numpy() - want)
+    assert np.all(off <= bound), float((off / bound).max())
+    off = np.abs(lse[:rows].double().cpu().numpy() - want_lse)
+    assert np.all(off <= dx + 2 * C.F32 * np.abs(want_lse)), float((off / dx).max())
+    first = out.clone()
+    assert torch.equal(att(q, out), first)
 
 
 @pytest.mark.gpu
