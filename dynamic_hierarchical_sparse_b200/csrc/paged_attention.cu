@@ -41,9 +41,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // and end; 32 + 8 heads of 128, page 16, up to 512 own keys, one kernel / two, in
 // us: 16 sequences on 1024 keys 15.5 / 22.5, on 16384 36.1 / 36.0, 32 on 2048
 // 22.9 / 30.2, on 8192 37.6 / 35.0, 12 on 32768 53.8 / 47.5, 32 on 32768 100 /
-// 57.7, 64 on 131072 587 / 188; 64 of d 64 on 1024 22.6 / 28.3, 16 of d 256 on
+// 58.8, 64 on 131072 587 / 193; 64 of d 64 on 1024 22.6 / 28.3, 16 of d 256 on
 // 8000 50.5 / 40.7; 12 sequences of 5 tokens in two groups, 8 + 4 heads of 256,
-// on 4097 50.1 / 38.5.
+// on 4097 50.1 / 39.4.  In all of these the table has room for what is held and no
+// more.  With room for 131072 tokens the rule takes the second kernel at any length,
+// and short prefixes lose by it: 16 sequences on 1024 keys 23.0 instead of 15.6, on
+// 4096 27.4 instead of 21.6, 32 on 2048 30.7 instead of 23.6.  One group with more
+// than 32 rows takes all groups' prefixes there.
 constexpr int kOwnPrefixRows = 32;
 constexpr long long kOwnPrefixWork = 1ll << 30;
 
@@ -823,6 +827,9 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
 // looked up, when the kernel before ends.  The whole call with 4 / 1, in us: 128
 // rows 9.3 / 11.1, 512 rows 15.6 / 17.1, 1024 rows 57.6 / 61.9, 1536 rows 138.4 /
 // 136.3, 2048 rows 187.0 / 187.9.
+// What it reads before it waits (offsets, lengths, groups) is the call's input, which
+// the kernel that let it start does not write, and which is complete: that kernel had
+// waited for the one before it, or was itself let start by the prefixes' kernel, which had.
 template <int N>
 struct __align__(N >= 4 ? 16 : 8) Cols {  // consecutive numbers, read and written together
   float x[N];

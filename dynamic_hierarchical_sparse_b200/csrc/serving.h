@@ -11,7 +11,8 @@
 
 namespace dhsa {
 
-// n / d for 0 <= n < 2^31 by a product and a shift (a division by a number that
+// n / d for 0 <= n < 2^31 by a product and a shift, the division by invariant
+// integers of Granlund and Montgomery (1994) (a division by a number that
 // is not known when compiling takes some forty instructions, which the first
 // pass over a kernel's code, the whole of a short call, pays for in fetching).
 struct FastDiv {

@@ -458,6 +458,8 @@ typedef struct {
  * through the table row of the group's first sequence; they have to be stored
  * there, also where kv_lens is shorter.  A prefix may end inside a page.
  * num_groups 0 (the three group pointers NULL): nothing is shared.
+ * max_pages is also what a call goes by for how long a prefix may be when it
+ * chooses its kernels: a table much wider than its prefixes costs short ones some us.
  * kv_lens, block_table and prefix_lens are read on the device by every call, so
  * a captured call follows their new contents; what is wrong in them (lengths
  * and prefix lengths outside 0 .. max_pages * page_size, pages outside the cache;
@@ -509,8 +511,8 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * and keys that a row does not see (of later tokens, of a shared prefix behind its
  * sequence's end, of slots not written yet) change nothing in it, whatever they
  * hold; infinities and NaN that it sees count as in plain arithmetic (a logit of
- * -infinity has no weight, one of +infinity makes the row NaN).  Rows that meet some
- * not finite are slow.  Results are the same from call to call.  A batch whose tables
+ * -infinity has no weight, one of +infinity makes the row NaN; an infinite value
+ * under a weight that is rounded to 0 is NaN).  Rows that meet some not finite are slow.  Results are the same from call to call.  A batch whose tables
  * leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
  * 32 keys is refused as DHSA_ERR_UNSUPPORTED.
  *   q, out     [T, Hq, d] in the cache's dtype; must not overlap
