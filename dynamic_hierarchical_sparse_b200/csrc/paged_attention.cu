@@ -195,16 +195,6 @@ __device__ __forceinline__ bool compute_sync_or(bool x) {
   return r != 0;
 }
 
-// The end of a piece on the four compute warps: joins the WN warps of each row
-// group, a quarter of the columns at a time, in the order of the warps, and
-// leaves the piece's partial.  o: m16n8 fragments of the warp's 16 rows.  false: a
-// warp's wait gave up.  With kFew rows or fewer (a decode step of as many query heads
-// a KV head) all columns go at once, two barriers instead of nine: 8 unshared
-// sequences 11.2 -> 10.8 us, of d 64 7.5 -> 7.2, two answers of d 256 9.7 -> 9.3, of
-// fp32 12.7 -> 12.3 (a call that has both kinds, 4 answers to 2500 tokens, 13.7 ->
-// 13.9: more code to fetch).
-constexpr int kFew = 4;
-
 // Storage types of the pages, and which partials are made again (see paged_rows_again).
 struct Bf16Pages {
   using K = __nv_bfloat16;
@@ -228,6 +218,15 @@ __device__ __forceinline__ bool close_piece(const PagedWork& w, const Walk& k, i
   return true;
 }
 
+// The end of a piece on the four compute warps: joins the WN warps of each row
+// group, a quarter of the columns at a time, in the order of the warps, and
+// leaves the piece's partial.  o: m16n8 fragments of the warp's 16 rows.  false: a
+// warp's wait gave up.  With kFew rows or fewer (a decode step of as many query heads
+// a KV head) all columns go at once, two barriers instead of nine: 8 unshared
+// sequences 11.2 -> 10.8 us, of d 64 7.5 -> 7.2, two answers of d 256 9.7 -> 9.3, of
+// fp32 12.7 -> 12.3 (a call that has both kinds, 4 answers to 2500 tokens, 13.7 ->
+// 13.9: more code to fetch).
+constexpr int kFew = 4;
 template <int D, typename C, typename P, int kMax, int WM, int WN, typename Walk>
 __device__ __forceinline__ bool finish_piece(const PagedWork& w, const Walk& k, const Ring& ctx, float (&o)[D / 8][4],
                                              const float (&m)[2], float (&l)[2], bool ok) {
@@ -611,12 +610,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
 // it has them all: h + l is x to 2^-23, and a b = h h' + h l' + l h' to about 2^-21
 // of |a b|, accumulated in fp32.  The split takes integer instructions, which takes
 // 4 sequences on 14117 keys from 74 to 64 us with d 256 and from 42 to 38 with d
-// 128 against the conversion's own; an infinity, and a
-// number that rounds to one, has no l that adds up to it (its products cancel to NaN, and
-// the row is made again, see paged_rows_again), and a NaN whose bits the rounding carries
-// past the sign leaves itself in l.  (The same in FFMA is
-// bound by shared memory: 16 rows are too few for a register block that would feed
-// it.)  A tile is 16 rows and 32 keys; the four warps split the keys.
+// 128 against the conversion's own.  An infinity, and a number that rounds to one, has
+// no l that adds up to it: its products cancel to NaN, and the row is made again (see
+// paged_rows_again).  A NaN whose bits the rounding carries past the sign leaves
+// itself in l.  (The same in FFMA is bound by shared memory: 16 rows are too few for
+// a register block that would feed it.)  A tile is 16 rows and 32 keys; the four
+// warps split the keys.
 constexpr int kFBN = 32;    // keys a tile
 constexpr int kFRows = 16;  // rows a tile
 

@@ -125,7 +125,7 @@ def test_long_contexts_closely(name):
     st.v_pages += 1.0
     q, rows = st.q.cuda(), st.cu[-1]
     att = api.PagedAttention(st.cache(), st.batch(), st.hq)
-    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    out, lse = torch.zeros_like(q), torch.empty(q.shape[:2], device="cuda")
     att(q, out, lse=lse)
     assert att.status() == 0
     want, want_lse, mean = T.want(st, "cuda")
