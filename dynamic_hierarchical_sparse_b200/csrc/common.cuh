@@ -87,7 +87,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // As mbar_wait below, but polls with test_wait instead of try_wait: the
 // thread is never suspended, so it sees a completed phase within a few
 // cycles.  For the one thread whose reaction time is on the critical path.
-template <bool kHeed = true>
 __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity,
                                                volatile int* abort_flag, uint32_t* status,
                                                unsigned long long limit_ns = kWaitLimitNs) {
@@ -97,7 +96,7 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity,
     if (mbar_test_wait(bar, parity)) return true;
     if ((it & 255u) == 0u) {
       if (*abort_flag) return false;
-      if (kHeed && status != nullptr && (*reinterpret_cast<volatile uint32_t*>(status) & kDevTimeout)) {
+      if (status != nullptr && (*reinterpret_cast<volatile uint32_t*>(status) & kDevTimeout)) {
         *abort_flag = 1;
         return false;
       }
@@ -113,9 +112,7 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity,
 // Waits for the phase with the given parity to complete.  Gives up when the
 // CTA-wide abort flag is set, when another CTA has already recorded a timeout
 // in the global status word, or after limit_ns, setting the flag and the
-// timeout bit.  Returns false when it gave up.  kHeed false: the status word is
-// only written (calls that do not clear it would find an earlier call's timeout).
-template <bool kHeed = true>
+// timeout bit.  Returns false when it gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
                                           volatile int* abort_flag, uint32_t* status,
                                           unsigned long long limit_ns = kWaitLimitNs) {
@@ -125,7 +122,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0u) {
       if (*abort_flag) return false;
-      if (kHeed && status != nullptr && (*reinterpret_cast<volatile uint32_t*>(status) & kDevTimeout)) {
+      if (status != nullptr && (*reinterpret_cast<volatile uint32_t*>(status) & kDevTimeout)) {
         *abort_flag = 1;
         return false;
       }
@@ -136,14 +133,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
       }
     }
   }
-}
-
-// mbar_wait<kHeed> by a whole warp with one answer: where a lane gives up, all do, and the
-// warp goes on together (votes and shuffles behind a wait count on all its lanes).
-template <bool kHeed = true>
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                               uint32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait<kHeed>(bar, parity, abort_flag, status));
 }
 
 // ------------------------------------------------------------------- TMA

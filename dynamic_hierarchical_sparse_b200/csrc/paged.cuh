@@ -24,8 +24,24 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 }
 
 // Waits of these kernels are on their own CTA's warps and copies.  One that runs out
-// is reported, ends its CTA's work and no other's, and nothing of it is kept: the status
-// word gathers reports across calls, so no wait looks there (mbar_wait<false>).
+// sets the CTA's abort flag, which ends the CTA's work and no other's, and is reported
+// at the end (report_abort).  The status word gathers reports across calls, so no wait
+// looks there: they get none to look at.
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, abort_flag, nullptr);
+}
+__device__ __forceinline__ bool paged_wait_spin(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait_spin(bar, parity, abort_flag, nullptr);
+}
+// By a whole warp with one answer: where a lane gives up, all do, and the warp goes on
+// together (votes and shuffles behind a wait count on all its lanes).
+__device__ __forceinline__ bool paged_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, paged_wait(bar, parity, abort_flag));
+}
+// By every warp (or a thread behind a barrier of all) that has done its last wait.
+__device__ __forceinline__ void report_abort(volatile int* abort_flag, uint32_t* status) {
+  if (*abort_flag) report(status, kDevTimeout);
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 

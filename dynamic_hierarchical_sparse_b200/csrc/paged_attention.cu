@@ -153,7 +153,7 @@ __device__ __forceinline__ void page_producer(const PagedWork& w, Walk& walk, co
       const int page_next = page_at(kt + 1);
       const int s = ring.stage;
       if (issued >= kStages)
-        ok = mbar_wait_warp<false>(bar_empty<kStages>(ring, s), ring.phase ^ 1u, ring.abort_flag, w.status);
+        ok = paged_wait_warp(bar_empty<kStages>(ring, s), ring.phase ^ 1u, ring.abort_flag);
       if (!ok) break;
       const unsigned active = __ballot_sync(0xffffffffu, page >= 0);
       if (lane == 0) mbar_arrive_expect_tx(bar_full(ring, s), __popc(active) * box * 128);
@@ -171,7 +171,7 @@ __device__ __forceinline__ void page_producer(const PagedWork& w, Walk& walk, co
     // let copies already in flight land before the CTA exits (bounded)
     volatile int never = 0;
     for (int x = max(0, issued - kStages); x < issued; ++x)
-      mbar_wait<false>(bar_full(ring, x % kStages), (x / kStages) & 1, &never, nullptr, 10000000ull);
+      mbar_wait(bar_full(ring, x % kStages), (x / kStages) & 1, &never, nullptr, 10000000ull);
   }
 }
 
@@ -422,7 +422,7 @@ __device__ __forceinline__ bool mma_piece(const PagedWork& w, const PagedWalk<kB
 
   bool ok = true;  // a warp whose wait gave up still takes part in the barriers below
   for (int kt = 0; kt < k.count; ++kt) {
-    ok = mbar_wait_warp<false>(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag, w.status);
+    ok = paged_wait_warp(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag);
     if (!ok) break;
     const uint32_t sk = ctx.sbase + ctx.stage * 2 * C::kTileBytes, sv = sk + C::kTileBytes;
     const int tile0 = (k.first + k.kt + kt) * kBN;
@@ -601,6 +601,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaCfg<D>::kCtas)
       }
     } while (ok && walk.next());
   }
+  report_abort(ctx.abort_flag, w.status);
   wait_for_previous();  // the prefixes' kernel, see open_list
 }
 
@@ -698,7 +699,7 @@ __device__ __forceinline__ bool f32_piece(const PagedWork& w, const PagedWalk<kF
   compute_sync<128>();  // Q is there
   bool ok = true;  // a warp whose wait gave up still takes part in the barriers at the end
   for (int kt = 0; kt < k.count; ++kt) {
-    ok = mbar_wait_warp<false>(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag, w.status);
+    ok = paged_wait_warp(bar_full(ctx, ctx.stage), ctx.phase, ctx.abort_flag);
     if (!ok) break;
     const uint32_t sk = ctx.sbase + ctx.stage * 2 * C::kTileBytes, sv = sk + C::kTileBytes;
     const int key0 = (k.first + k.kt + kt) * kFBN + r0;
@@ -815,6 +816,7 @@ __global__ void __launch_bounds__(kMmaThreads, F32Cfg<D>::kCtas)
     while (f32_piece<D>(w, walk, ctx) && walk.next()) {
     }
   }
+  report_abort(ctx.abort_flag, w.status);
 }
 
 // ------------------------------------------------------------------ join

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           const int page_next = page_at(kt + 1);
           const unsigned bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128;
           const int in_page = ((walk.first + walk.kt + kt) * kBN + pp * box) & (ps - 1);
-          if (round > 0) ok = mbar_wait_warp<false>(bar(free + slot), (round - 1) & 1, abort_flag, w.status);
+          if (round > 0) ok = paged_wait_warp(bar(free + slot), (round - 1) & 1, abort_flag);
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), bytes);
           __syncwarp();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // let copies already in flight land before the CTA exits (bounded)
         volatile int never = 0;
         for (int x = max(0, issued - stages); x < issued; ++x)
-          mbar_wait<false>(bar(full + x % stages), (x / stages) & 1, &never, nullptr, 10000000ull);
+          mbar_wait(bar(full + x % stages), (x / stages) & 1, &never, nullptr, 10000000ull);
       }
     } else if (work && warp < C::kMma + C::kLanes) {
       // ------------------------------------------------------------- MMA
@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // turn x (counted across pieces): lane 1 waits for lane 0's turn x, lane 0 for lane 1's turn x - 1
         auto wait_turn = [&](int x) -> bool {
           if (C::kLanes == 1) return true;
-          if (a == 1) return mbar_wait_spin<false>(bar(kBarTurn + 0), x & 1, abort_flag, w.status);
-          return x == 0 || mbar_wait_spin<false>(bar(kBarTurn + 1), (x - 1) & 1, abort_flag, w.status);
+          if (a == 1) return paged_wait_spin(bar(kBarTurn + 0), x & 1, abort_flag);
+          return x == 0 || paged_wait_spin(bar(kBarTurn + 1), (x - 1) & 1, abort_flag);
         };
         auto end_turn = [&]() {
           if (C::kLanes == 2) mbar_arrive(bar(kBarTurn + a));
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           const int step = ap ? 2 : 1, kt0 = ap ? a : 0;
           // one turn for the first S, then one for each of the tiles (of the lane that has more)
           const int turns = 1 + (ap ? (walk.count + 1) / 2 : walk.count);
-          ok = mbar_wait<false>(bar(kBarQFull + a), piece & 1, abort_flag, w.status);
+          ok = paged_wait(bar(kBarQFull + a), piece & 1, abort_flag);
           // turn x: P V of the lane's tile x - 1 and S of its tile x
           for (int x = 0; ok && x < turns; ++x, ++turn) {
             const int kt = kt0 + (x - 1) * step;  // of P V
@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             const int np = n0 + kt, ns = np + step;
             const int vs = np % C::kVStages, ks = ns % C::kKStages;
             auto k_there = [&]() {
-              return mbar_wait_spin<false>(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag, w.status);
+              return paged_wait_spin(bar(kBarKFull + ks), (ns / C::kKStages) & 1, abort_flag);
             };
             auto p_there = [&]() {
-              return mbar_wait_spin<false>(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag, w.status) &&
-                     mbar_wait_spin<false>(bar(kBarPHalf + p_bar(a, mine)), p_phase(mine), abort_flag, w.status);
+              return paged_wait_spin(bar(kBarVFull + vs), (np / C::kVStages) & 1, abort_flag) &&
+                     paged_wait_spin(bar(kBarPHalf + p_bar(a, mine)), p_phase(mine), abort_flag);
             };
             auto send_s = [&]() {
               const uint32_t kbase = sbase + C::kOffK + ks * C::kTile, tS = tS0 + kBN * p_bar(a, ns);
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk) {
                 if (kk == kBN / 32) {
-                  if (!mbar_wait_spin<false>(bar(kBarPFull + p_bar(a, mine)), p_phase(mine), abort_flag, w.status))
+                  if (!paged_wait_spin(bar(kBarPFull + p_bar(a, mine)), p_phase(mine), abort_flag))
                     return false;
                   tc_fence_after();
                 }
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // every MMA issued above completes before TMEM is released
         umma_commit(bar(kBarDrain + a));
         volatile int never = 0;
-        mbar_wait<false>(bar(kBarDrain + a), 0, &never, nullptr);
+        mbar_wait(bar(kBarDrain + a), 0, &never, nullptr);
       }
     }
   } else {
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int k0 = (first + kt) * kBN, pb = p_bar(a, mine);
         const uint32_t tS = tS0 + kBN * pb;
         if (!rehearsal) {
-          if (!(ok = mbar_wait_warp<false>(bar(kBarSFull + pb), p_phase(mine), abort_flag, w.status))) break;
+          if (!(ok = paged_wait_warp(bar(kBarSFull + pb), p_phase(mine), abort_flag))) break;
           ++mine;
           tc_fence_after();
           if (k0 + kBN > hi) {
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             // NaN is NaN: V's rows there are zeroed (a thread a row; lanes that share
             // the tile write the same zeros)
             const int n = n0 + kt, s = n % C::kVStages;
-            if (!(ok = mbar_wait_warp<false>(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag, w.status))) break;
+            if (!(ok = paged_wait_warp(bar(kBarVFull + s), (n / C::kVStages) & 1, abort_flag))) break;
             if (row < kBN && k0 + row >= hi) {
 #pragma unroll 1
               for (int c = 0; c < D / 8; ++c)
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           // done, since this S was issued after them (with one lane: waited for)
           if (C::kLanes == 1 && !rehearsal) {
             const int n = n0 + kt - 1;
-            ok = mbar_wait_warp<false>(bar(kBarVFree + n % C::kVStages), (n / C::kVStages) & 1, abort_flag, w.status);
+            ok = paged_wait_warp(bar(kBarVFree + n % C::kVStages), (n / C::kVStages) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
           }
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       const bool more = walk.next();
       if (more) send_q(walk);
       if (some) {
-        if (!(ok = mbar_wait_warp<false>(bar(kBarODone + a), done[a] & 1, abort_flag, w.status))) break;
+        if (!(ok = paged_wait_warp(bar(kBarODone + a), done[a] & 1, abort_flag))) break;
         tc_fence_after();
       }
       if (!ap) {
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarCross + a));
-        if (!(ok = mbar_wait_warp<false>(bar(kBarCross + 1 - a), joins & 1, abort_flag, w.status))) break;
+        if (!(ok = paged_wait_warp(bar(kBarCross + 1 - a), joins & 1, abort_flag))) break;
         tc_fence_after();
         if (warp_valid) {
           uint32_t xm, xl;
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         // no product of the next piece starts before both lanes have read TMEM
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPiece));
-        if (!(ok = mbar_wait_warp<false>(bar(kBarPiece), (done[0]) & 1, abort_flag, w.status))) break;
+        if (!(ok = paged_wait_warp(bar(kBarPiece), (done[0]) & 1, abort_flag))) break;
       } else {
         if (!more) break;
       }
@@ -717,6 +717,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == C::kMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0) report_abort(abort_flag, w.status);
 }
 
 template <int D>

@@ -32,28 +32,38 @@ def test_waits(name):
     lines = _lines(name)
     warp = 0
     for i, line in enumerate(lines):
-        if re.search(r"\bmbar_wait_warp\b", line):
+        if "paged_wait_warp(" in line:
             warp += 1
             assert not any("lane == 0" in c for c in _branch(lines, i)), line
-        if re.search(r"\bmbar_wait(?:_spin)?(?:<\w+>)?\(", line):
+        if re.search(r"\b(?:paged|mbar)_wait(?:_spin)?\(", line):
             lone = any("lane == 0" in c for c in _branch(lines, i))
             dropped = "&never" in line
             assert lone or dropped, (i + 1, line)
     assert warp >= 3
 
 
-@pytest.mark.parametrize("name", ["paged_attention.cu", "paged_prefix.cu"])
+@pytest.mark.parametrize("name", ["paged_attention.cu", "paged_prefix.cu", "paged.cuh"])
 def test_no_wait_goes_by_an_earlier_calls_report(name):
-    """The status word of these calls is not cleared by them, so no wait may end by what it says."""
-    for line in _lines(name):
-        for wait in re.findall(r"\bmbar_wait\w*(?:<\w+>)?\(", line):
-            assert wait.endswith("<false>("), line
-    text = open(os.path.join(CSRC, "common.cuh")).read()
-    reads = re.findall(r"if \((.*)reinterpret_cast<volatile uint32_t\*>\(status\)", text)
-    assert len(reads) == 2 and all(r.startswith("kHeed && ") for r in reads)
+    """The status word of these calls is not cleared by them, so no wait may end by what it says: the waits that
+    read it are given none."""
+    waits = [line for line in _lines(name) if re.search(r"\bmbar_wait(?:_spin)?\(", line)]
+    for line in waits:
+        assert "&never, nullptr" in line or "abort_flag, nullptr)" in line, line
+    assert len(waits) >= 1
+
+
+def test_a_wait_that_ran_out_is_reported_at_the_end():
+    """Each kernel with waits looks at its CTA's abort flag behind the last of them."""
+    for name, kernels in (("paged_attention.cu", 2), ("paged_prefix.cu", 1)):
+        text = open(os.path.join(CSRC, name)).read()
+        ends = [text[m.start():] for m in re.finditer(r"^__global__ .*\n(?:.*\n)?.*paged_(?:mma|f32|prefix)_kernel\(", text, re.M)]
+        assert len(ends) == kernels
+        for body in ends:
+            body = body[:body.index("\n}\n")]
+            assert "report_abort(" in body and "wait(" not in body[body.index("report_abort("):]
 
 
 def test_the_warp_wait_votes():
-    text = open(os.path.join(CSRC, "common.cuh")).read()
-    body = text[text.index("bool mbar_wait_warp("):]
-    assert re.search(r"return __all_sync\(0xffffffffu, mbar_wait\b", body[:body.index("\n}")])
+    text = open(os.path.join(CSRC, "paged.cuh")).read()
+    body = text[text.index("bool paged_wait_warp("):]
+    assert re.search(r"return __all_sync\(0xffffffffu, paged_wait\(", body[:body.index("\n}")])
