@@ -384,7 +384,8 @@ typedef struct {
  * The table holds f_i / (2 pi) as a 64-bit binary fraction of a turn, rounded, and
  * position times fraction is integer arithmetic modulo one turn, so angles stay right
  * at every position: within 2^-32 turns from taking the top 32 bits, plus |p| 2^-63
- * for frequencies up to 1 (2^-64 (1/2 + |f_i|) |p| for given ones).  cos, sin and the rotation are fp32, each output rounded once. */
+ * for frequencies up to 1 (2^-64 (1/2 + |f_i|) |p| for given ones).  cos, sin and the
+ * rotation are fp32, each output rounded once. */
 #define DHSA_ROPE_MAX_PAIRS 128
 typedef enum {
   DHSA_ROPE_UNSCALED = 0,
@@ -512,8 +513,10 @@ DHSA_API dhsa_status dhsa_kv_append(const dhsa_paged_cache* cache, const dhsa_pa
  * sequence's end, of slots not written yet) change nothing in it, whatever they
  * hold; infinities and NaN that it sees count as in plain arithmetic (a logit of
  * -infinity has no weight, one of +infinity makes the row NaN; an infinite value
- * under a weight that is rounded to 0 is NaN).  Rows that meet some not finite are slow.  Results are the same from call to call.  A batch whose tables
- * leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
+ * under a weight that is rounded to 0 is NaN).  Rows that meet some not finite are
+ * slow (up to some 0.3 us a key and row; where one CTA's share is millions of them,
+ * a wait of its others may run out, DHSA_ERR_TIMEOUT).  Results are the same from
+ * call to call.  A batch whose tables leave room for 2^30 or more tiles of 16 query rows (tokens times Hq / Hkv) and
  * 32 keys is refused as DHSA_ERR_UNSUPPORTED.
  *   q, out     [T, Hq, d] in the cache's dtype; must not overlap
  *   lse        device fp32 [T, Hq] contiguous, or NULL
